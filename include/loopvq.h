@@ -63,7 +63,10 @@ enum {
   LOOPVQ_ENCODE_STATUS_UNDRAINED = 2,
   /* a slot_mapping entry at or past n_pages * page_tokens: that token was
    * not written */
-  LOOPVQ_ENCODE_STATUS_BAD_SLOT = 4
+  LOOPVQ_ENCODE_STATUS_BAD_SLOT = 4,
+  /* a sequence of a loopvq_append call that is shorter than its appended
+   * rows, or reaches past the rotation table: none of its rows was written */
+  LOOPVQ_ENCODE_STATUS_BAD_POSITION = 8
 };
 
 /* Flag bits of a decode call's status word (the first int32 of its
@@ -221,9 +224,9 @@ loopvq_status loopvq_encode(const loopvq_config* cfg, int layer, int loop_group_
 
 /*
  * Reads the encoder status word of the current device into *flags
- * (LOOPVQ_ENCODE_STATUS_* bits that any loopvq_encode, loopvq_encode_evict or
- * loopvq_kmeans_step kernel set since the word was last cleared) and clears
- * it when `clear` is nonzero. This call synchronises with the device (it
+ * (LOOPVQ_ENCODE_STATUS_* bits that any loopvq_encode, loopvq_encode_evict,
+ * loopvq_kmeans_step or loopvq_append kernel set since the word was last
+ * cleared) and clears it when `clear` is nonzero. This call synchronises with the device (it
  * copies a device word to the host). A word of zero means every encode so
  * far wrote all of its indices.
  */
@@ -248,6 +251,78 @@ loopvq_status loopvq_encode_status(int* flags, int clear);
 loopvq_status loopvq_encode_evict(const loopvq_config* cfg, int n_tokens, const void* x,
                                   const float* codebooks, const int64_t* slot_mapping,
                                   uint8_t* pool, void* stream);
+
+/*
+ * Appends new tokens to the bf16 windows of (layer, loop_step), rotates
+ * their queries and keys by position on the way, and stages the tokens that
+ * the windows push out for the encoder (airadar.tv, section "Utilisation":
+ * the first PREFIX_TOKENS and the latest RECENT_TOKENS tokens stay in bf16).
+ * One call does what a serving program does between its q/k/v projection and
+ * loopvq_decode_attn (one token per sequence) or its prompt attention (a
+ * chunk of tokens per sequence).
+ *
+ * Row r of the call is token i = r - s of sequence b, where the sequence has
+ * the rows [s, s + n): s = token_starts[b], n = token_starts[b+1] - s, or
+ * s = b, n = 1 when token_starts is NULL. Its position is p = N - n + i with
+ * N = seq_lens[b], the sequence's length counting the appended tokens (the
+ * same array that the attention calls read afterwards). Then
+ *   q_out[r] = rot(q[r], p);  k' = rot(k[r], p);  v' = v[r];
+ *   a token p < P goes to window slot p, a token p >= max(P, N - R) to slot
+ *   P + (p - P) mod R;
+ *   the token e = p - R that row r pushes out (when e >= P) goes to row r of
+ *   the staging slices, from the window if it was cached before the call,
+ *   from row r - R of the call otherwise;
+ *   slot_mapping[r] = block_table[b][v / Pg]*Pg + v % Pg for v = e - P, or
+ *   -1 when row r pushes nothing out.
+ * The staged rows and slot_mapping are what loopvq_encode_evict (up to 64
+ * rows) and loopvq_encode (any number) take once the loop group's steps are
+ * complete. Rows without a sequence (behind the last token_starts entry, or
+ * of a sequence with seq_lens[b] <= 0: a padded batch) write nothing but
+ * slot_mapping[r] = -1; staging rows that nothing was pushed into keep their
+ * contents.
+ *
+ * rot(x, p) turns each pair (a, b) of the first rot_dim channels by row p of
+ * the table, (a cos - b sin, b cos + a sin), in float32 with one rounding to
+ * bf16; pair i is channels (i, i + rot_dim/2), or (2i, 2i + 1) when
+ * interleaved is nonzero. Other channels are copied.
+ *
+ *  q, k, v       bf16, token r's heads dense at base + r*token_stride
+ *                ([Hq][d] and [Hkv][d]; strides in elements, multiples of 8;
+ *                16-byte aligned bases), e.g. three slices of one fused
+ *                projection. q and q_out may both be NULL.
+ *  rope          float32 [n_positions][rot_dim]: row p holds the rot_dim/2
+ *                cosines, then the rot_dim/2 sines of position p; 16-byte
+ *                aligned. NULL (with n_positions and rot_dim 0) appends keys
+ *                that need no rotation, e.g. staged rows put back.
+ *  rot_dim       0, or a multiple of 4 up to d (a multiple of 16 takes the
+ *                16-byte form of the kernel).
+ *  token_starts  int32 [batch + 1], ascending, in [0, n_tokens]; or NULL
+ *                with n_tokens == batch.
+ *  seq_lens      int32 [batch].
+ *  win_k/win_v   bf16 [batch][Hkv][P+R][d] of (layer, loop_step), read and
+ *                written.
+ *  q_out         bf16 [n_tokens][Hq][d]. May equal q when q is dense.
+ *  evicted       base of the staging buffer bf16 [L][G][2][g][n_tokens][Hkv][d]
+ *                of loopvq_encode_evict; this call writes rows of the slices
+ *                (layer, loop_step / g, K and V, loop_step % g) only.
+ *  slot_mapping  int64 [n_tokens], or NULL: the slots are the same for every
+ *                layer and loop step, so one call of a step writes them.
+ *  block_table   int32 [batch][max_pages_per_seq]; may be NULL when
+ *                slot_mapping is.
+ * Buffers that the call writes must not overlap each other or its inputs
+ * (q_out and q apart). A sequence shorter than its rows, or longer than
+ * n_positions, is skipped and sets LOOPVQ_ENCODE_STATUS_BAD_POSITION; a page
+ * outside the table or the pool gives slot -1 and sets
+ * LOOPVQ_ENCODE_STATUS_BAD_SLOT (loopvq_encode_status reads both).
+ * n_tokens == 0 is a no-op that returns LOOPVQ_OK.
+ */
+loopvq_status loopvq_append(const loopvq_config* cfg, int layer, int loop_step, int batch,
+                            int n_tokens, const void* q, int64_t q_token_stride, const void* k,
+                            int64_t k_token_stride, const void* v, int64_t v_token_stride,
+                            const float* rope, int n_positions, int rot_dim, int interleaved,
+                            const int32_t* token_starts, const int32_t* seq_lens,
+                            const int32_t* block_table, void* win_k, void* win_v, void* q_out,
+                            void* evicted, int64_t* slot_mapping, void* stream);
 
 /*
  * One weighted k-means (Lloyd) step on the codebooks of (layer,

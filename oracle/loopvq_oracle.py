@@ -498,3 +498,42 @@ def unpack_pages(page_array: np.ndarray, pages: list[int], n: int,
             idx_K[v, j] = page_array[pg, 0, plane_offset(slot, j, J, 0)]
             idx_V[v, j] = page_array[pg, 1, plane_offset(slot, j, J, 1, page_tokens)]
     return idx_K, idx_V
+
+
+# ---------------------------------------------------------------------------
+# Appending tokens to the windows
+# ---------------------------------------------------------------------------
+def rotate_ref(x: np.ndarray, cos: np.ndarray, sin: np.ndarray, interleaved: bool) -> np.ndarray:
+    """Rotate the first ``2*len(cos)`` entries of ``x [..., d]`` pair by pair:
+    ``(a, b) -> (a cos - b sin, b cos + a sin)``. Pair ``i`` is entries
+    ``(i, i + n)``, or ``(2i, 2i + 1)`` when interleaved."""
+    n = len(cos)
+    y = np.array(x, dtype=np.float64)
+    for i in range(n):
+        a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + n)
+        y[..., a] = x[..., a] * cos[i] - x[..., b] * sin[i]
+        y[..., b] = x[..., b] * cos[i] + x[..., a] * sin[i]
+    return y
+
+
+def append_sequence_ref(window: np.ndarray, tokens: np.ndarray, length: int, prefix: int,
+                        recent: int) -> dict[int, tuple[int, np.ndarray]]:
+    """Append ``tokens [n][H][d]`` one by one to ``window [H][P+R][d]`` (in
+    place) of a sequence whose length counting them is ``length``. Returns,
+    for each row that pushes a token out of the recent window, the pushed-out
+    token's position and value ``[H][d]``."""
+    gone = {}
+    n = len(tokens)
+    for i in range(n):
+        p = length - n + i
+        if p < prefix:
+            window[:, p] = tokens[i]
+            continue
+        if recent == 0:
+            gone[i] = (p, np.array(tokens[i]))
+            continue
+        slot = prefix + (p - prefix) % recent
+        if p - recent >= prefix:
+            gone[i] = (p - recent, np.array(window[:, slot]))
+        window[:, slot] = tokens[i]
+    return gone

@@ -8,6 +8,7 @@ from .binding import (  # noqa: F401
     LOOPVQ_DECODE_STATUS_BAD_PAGE,
     LOOPVQ_ENCODE_STATUS_TIMEOUT,
     LOOPVQ_ENCODE_STATUS_UNDRAINED,
+    LOOPVQ_ENCODE_STATUS_BAD_POSITION,
     LOOPVQ_ENCODE_STATUS_BAD_SLOT,
     LOOPVQ_DECODE_STATUS_RANGE,
     LOOPVQ_DECODE_STATUS_SHARED_BASE,
@@ -18,6 +19,7 @@ from .binding import (  # noqa: F401
     LoopVQConfig,
     LOOPVQ_STATIC_SCRATCH_BYTES,
     LoopVQError,
+    loopvq_append,
     loopvq_bf16_decode_attn,
     loopvq_bf16_decode_workspace_bytes,
     loopvq_cache_layout,

@@ -30,6 +30,7 @@ LOOPVQ_DTYPE_F32 = 1
 LOOPVQ_ENCODE_STATUS_TIMEOUT = 1
 LOOPVQ_ENCODE_STATUS_UNDRAINED = 2
 LOOPVQ_ENCODE_STATUS_BAD_SLOT = 4
+LOOPVQ_ENCODE_STATUS_BAD_POSITION = 8
 LOOPVQ_DECODE_STATUS_BAD_PAGE = 1
 LOOPVQ_DECODE_STATUS_SHARED_BASE = 2
 LOOPVQ_DECODE_STATUS_RANGE = 4
@@ -87,6 +88,9 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.loopvq_encode_status.argtypes = [ctypes.POINTER(ctypes.c_int), I]
     lib.loopvq_encode_evict.restype = I
     lib.loopvq_encode_evict.argtypes = [cfgp, I, P, P, P, P, P]
+    lib.loopvq_append.restype = I
+    lib.loopvq_append.argtypes = [cfgp, I, I, I, I, P, I64, P, I64, P, I64, P, I, I, I, P, P, P, P,
+                                  P, P, P, P, P]
     lib.loopvq_prefill_workspace_bytes.restype = SZ
     lib.loopvq_prefill_workspace_bytes.argtypes = [cfgp, I, I, I]
     lib.loopvq_prefill_attn.restype = I
@@ -113,7 +117,7 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
 _lib = _load()
 
 EXPORTED = ("loopvq_status_string", "loopvq_cache_layout", "loopvq_encode", "loopvq_encode_evict",
-            "loopvq_encode_status", "loopvq_prefill_workspace_bytes", "loopvq_prefill_attn",
+            "loopvq_encode_status", "loopvq_append", "loopvq_prefill_workspace_bytes", "loopvq_prefill_attn",
             "loopvq_decode_workspace_bytes", "loopvq_decode_attn", "loopvq_decode_attn_noalloc",
             "loopvq_bf16_decode_workspace_bytes", "loopvq_bf16_decode_attn",
             "loopvq_kmeans_assign_bytes", "loopvq_kmeans_step")
@@ -234,6 +238,89 @@ def loopvq_encode_evict(cfg: LoopVQConfig, x: torch.Tensor, codebooks: torch.Ten
     st = _lib.loopvq_encode_evict(cfg.c_ref(), n, _ptr(x), _ptr(codebooks), _ptr(slot_mapping),
                                   _ptr(pool), _stream(stream))
     _check("loopvq_encode_evict", st)
+
+
+def _on_current_device(fn: str, *tensors) -> None:
+    """Every tensor (None apart) lies on the current CUDA device, whose
+    stream the call is enqueued on."""
+    for t in tensors:
+        if t is not None and not t.is_cuda:
+            raise ValueError(f"{fn}: tensors must be on a CUDA device")
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{fn}: a tensor is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+
+
+def _token_rows(name: str, x: torch.Tensor, heads: int, d: int) -> int:
+    """Token stride of a bf16 ``[n][heads][d]`` tensor with dense rows."""
+    if x.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be bfloat16")
+    if x.shape[1:] != (heads, d) or x.stride(2) != 1 or (heads > 1 and x.stride(1) != d):
+        raise ValueError(f"{name} must be [n_tokens][{heads}][{d}] with dense rows")
+    return x.stride(0) if x.shape[0] > 1 else 0
+
+
+def loopvq_append(cfg: LoopVQConfig, layer: int, loop_step: int, q: torch.Tensor | None,
+                  k: torch.Tensor, v: torch.Tensor, rope: torch.Tensor | None,
+                  seq_lens: torch.Tensor, win_k: torch.Tensor, win_v: torch.Tensor,
+                  q_out: torch.Tensor | None, evicted: torch.Tensor,
+                  token_starts: torch.Tensor | None = None, interleaved: bool = False,
+                  block_table: torch.Tensor | None = None, slot_mapping: torch.Tensor | None = None,
+                  stream=None) -> None:
+    """Appends n tokens to the windows of (layer, loop_step). q ``[n][Hq][d]``,
+    k, v ``[n][Hkv][d]`` bf16 (any token stride); rope float32
+    ``[positions][rot_dim]`` (cosines, then sines) or None; seq_lens int32
+    ``[B]`` counting the new tokens; win_k, win_v bf16 ``[B][Hkv][P+R][d]``;
+    q_out bf16 ``[n][Hq][d]``; evicted bf16 ``[L][G][2][g][n][Hkv][d]``;
+    token_starts int32 ``[B+1]`` or None (one token per sequence);
+    slot_mapping int64 ``[n]``, written (with block_table) when given."""
+    n, batch = k.shape[0], seq_lens.shape[0]
+    hq, hkv, d = cfg.n_q_heads, cfg.n_kv_heads, cfg.head_dim
+    qs = 0
+    if q is not None:
+        qs = _token_rows("q", q, hq, d)
+        if q.shape[0] != n:
+            raise ValueError("q and k must have the same number of tokens")
+        if q_out is None or q_out.dtype != torch.bfloat16 or q_out.shape != q.shape or \
+                not q_out.is_contiguous():
+            raise ValueError("q_out must be dense bfloat16 of q's shape")
+    ks, vs = _token_rows("k", k, hkv, d), _token_rows("v", v, hkv, d)
+    if v.shape[0] != n:
+        raise ValueError("k and v must have the same number of tokens")
+    slots = cfg.prefix_tokens + cfg.recent_tokens
+    for name, w in (("win_k", win_k), ("win_v", win_v)):
+        if w.dtype != torch.bfloat16 or w.shape != (batch, hkv, slots, d) or not w.is_contiguous():
+            raise ValueError(f"{name} must be dense bfloat16 [B][Hkv][P+R][d]")
+    if evicted.dtype != torch.bfloat16 or not evicted.is_contiguous() or evicted.numel() != \
+            cfg.n_layers * cfg.n_loops * 2 * n * hkv * d:
+        raise ValueError("evicted must be dense bfloat16 [L][G][2][g][n_tokens][Hkv][d]")
+    positions = rot = 0
+    if rope is not None:
+        if rope.dtype != torch.float32 or rope.dim() != 2 or not rope.is_contiguous():
+            raise ValueError("rope must be dense float32 [positions][rot_dim]")
+        positions, rot = rope.shape
+    if seq_lens.dtype != torch.int32 or not seq_lens.is_contiguous():
+        raise ValueError("seq_lens must be dense int32 [B]")
+    if token_starts is not None and (token_starts.dtype != torch.int32 or
+                                     not token_starts.is_contiguous() or
+                                     token_starts.shape[0] != batch + 1):
+        raise ValueError("token_starts must be dense int32 [B + 1]")
+    if slot_mapping is not None:
+        if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (n,) or \
+                not slot_mapping.is_contiguous():
+            raise ValueError("slot_mapping must be dense int64 [n_tokens]")
+        if block_table is None or block_table.dtype != torch.int32 or \
+                block_table.shape != (batch, cfg.max_pages_per_seq) or not block_table.is_contiguous():
+            raise ValueError("block_table must be dense int32 [B][max_pages_per_seq]")
+    _on_current_device("loopvq_append", q, k, v, rope, seq_lens, win_k, win_v, q_out, evicted,
+                       token_starts, block_table, slot_mapping)
+    st = _lib.loopvq_append(
+        cfg.c_ref(), layer, loop_step, batch, n, _ptr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+        _ptr(rope), positions, rot, int(interleaved), _ptr(token_starts), seq_lens.data_ptr(),
+        _ptr(block_table) if slot_mapping is not None else None, win_k.data_ptr(), win_v.data_ptr(),
+        _ptr(q_out) if q is not None else None, evicted.data_ptr(), _ptr(slot_mapping), _stream(stream))
+    _check("loopvq_append", st)
 
 
 def _xw_strides(x: torch.Tensor, w: torch.Tensor | None) -> tuple[int, int, int, int]:

@@ -225,6 +225,42 @@ loopvq_status loopvq_encode_evict(const loopvq_config* cfg, int n_tokens, const 
   return loopvq::launch_encode_evict(a);
 }
 
+loopvq_status loopvq_append(const loopvq_config* cfg, int layer, int loop_step, int batch,
+                            int n_tokens, const void* q, int64_t q_token_stride, const void* k,
+                            int64_t k_token_stride, const void* v, int64_t v_token_stride,
+                            const float* rope, int n_positions, int rot_dim, int interleaved,
+                            const int32_t* token_starts, const int32_t* seq_lens,
+                            const int32_t* block_table, void* win_k, void* win_v, void* q_out,
+                            void* evicted, int64_t* slot_mapping, void* stream) {
+  Geometry g;
+  loopvq_status st = loopvq::make_geometry(cfg, &g);
+  if (st != LOOPVQ_OK) return st;
+  if (layer < 0 || layer >= g.L || loop_step < 0 || loop_step >= g.T) return LOOPVQ_ERR_INVALID_ARG;
+  if (batch <= 0 || batch > g.max_batch || n_tokens < 0) return LOOPVQ_ERR_INVALID_ARG;
+  if (rot_dim < 0 || rot_dim > g.d || rot_dim % 2 != 0 || n_positions < 0) return LOOPVQ_ERR_INVALID_ARG;
+  if ((rot_dim > 0) != (rope != nullptr) || (rot_dim > 0 && n_positions == 0)) return LOOPVQ_ERR_INVALID_ARG;
+  if (rot_dim % 4 != 0) return LOOPVQ_ERR_UNSUPPORTED;
+  if (n_tokens == 0) return LOOPVQ_OK;
+  if (token_starts == nullptr && n_tokens != batch) return LOOPVQ_ERR_INVALID_ARG;
+  if (k == nullptr || v == nullptr || seq_lens == nullptr || evicted == nullptr) return LOOPVQ_ERR_INVALID_ARG;
+  if ((q == nullptr) != (q_out == nullptr)) return LOOPVQ_ERR_INVALID_ARG;
+  if (g.W > 0 && (win_k == nullptr || win_v == nullptr)) return LOOPVQ_ERR_INVALID_ARG;
+  if (slot_mapping != nullptr && block_table == nullptr) return LOOPVQ_ERR_INVALID_ARG;
+  if (q_token_stride < 0 || k_token_stride < 0 || v_token_stride < 0 || q_token_stride % 8 != 0 ||
+      k_token_stride % 8 != 0 || v_token_stride % 8 != 0)
+    return LOOPVQ_ERR_INVALID_ARG;
+  if (!loopvq::aligned(q, 16) || !loopvq::aligned(k, 16) || !loopvq::aligned(v, 16) ||
+      !loopvq::aligned(rope, 16) || !loopvq::aligned(token_starts, 4) || !loopvq::aligned(seq_lens, 4) ||
+      !loopvq::aligned(block_table, 4) || !loopvq::aligned(win_k, 16) || !loopvq::aligned(win_v, 16) ||
+      !loopvq::aligned(q_out, 16) || !loopvq::aligned(evicted, 16) || !loopvq::aligned(slot_mapping, 8))
+    return LOOPVQ_ERR_INVALID_ARG;
+  loopvq::AppendArgs a{&g,           layer,          loop_step, batch,          n_tokens,  q,
+                       q_token_stride, k,            k_token_stride, v,         v_token_stride, rope,
+                       n_positions,  rot_dim,        interleaved, token_starts, seq_lens,  block_table,
+                       win_k,        win_v,          q_out,     evicted,        slot_mapping, stream};
+  return loopvq::launch_append(a);
+}
+
 size_t loopvq_kmeans_assign_bytes(const loopvq_config* cfg, int n_tokens) {
   Geometry g;
   if (loopvq::make_geometry(cfg, &g) != LOOPVQ_OK || n_tokens < 0) return 0;

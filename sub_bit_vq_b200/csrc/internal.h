@@ -106,6 +106,31 @@ loopvq_status launch_encode_evict(const EncodeArgs& a);
 // elements whose weight sum is zero keep their value.
 loopvq_status launch_kmeans_update(const EncodeArgs& a, float* codebooks);
 
+// Appends the keys and values of new tokens to the windows of (layer,
+// loop_step), rotating q and k, and stages the tokens pushed out (append.cu).
+struct AppendArgs {
+  const Geometry* geo;
+  int layer, loop_step, batch, n_tokens;
+  const void* q;                 // or null: keys and values only
+  int64_t q_token_stride;
+  const void* k;
+  int64_t k_token_stride;
+  const void* v;
+  int64_t v_token_stride;
+  const float* rope;             // null when rot_dim is 0
+  int n_positions, rot_dim, interleaved;
+  const int32_t* token_starts;   // or null: one token per sequence
+  const int32_t* seq_lens;
+  const int32_t* block_table;    // used with slot_mapping only
+  void* win_k;
+  void* win_v;
+  void* q_out;
+  void* evicted;
+  int64_t* slot_mapping;         // or null
+  void* stream;
+};
+loopvq_status launch_append(const AppendArgs& a);
+
 struct Bf16DecodeArgs {
   int batch, Hq, Hkv, d, max_seq_len;
   const void* q;
