@@ -177,6 +177,8 @@ def _ptr(t) -> int | None:
 
 def _stream(stream) -> int | None:
     if stream is None:
+        if torch.cuda.is_initialized():   # the raw handle, without a Stream object
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -243,22 +245,35 @@ def loopvq_encode_evict(cfg: LoopVQConfig, x: torch.Tensor, codebooks: torch.Ten
 def _on_current_device(fn: str, *tensors) -> None:
     """Every tensor (None apart) lies on the current CUDA device, whose
     stream the call is enqueued on."""
+    dev = -1
     for t in tensors:
-        if t is not None and not t.is_cuda:
-            raise ValueError(f"{fn}: tensors must be on a CUDA device")
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{fn}: a tensor is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+        if t is not None:
+            i = t.get_device()
+            if i != dev or i < 0:
+                if i < 0:
+                    raise ValueError(f"{fn}: tensors must be on a CUDA device")
+                if i != torch._C._cuda_getDevice():
+                    raise ValueError(f"{fn}: a tensor is on cuda:{i}, which is not the current device")
+                dev = i
 
 
-def _token_rows(name: str, x: torch.Tensor, heads: int, d: int) -> int:
+def _dense(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple) -> int:
+    """Address of a dense tensor of the given type and shape."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be dense {dtype} {tuple(shape)}, not {t.dtype} {tuple(t.shape)}"
+                         f"{'' if t.is_contiguous() else ' with strides ' + str(t.stride())}")
+    return t.data_ptr()
+
+
+def _token_rows(name: str, x: torch.Tensor, shape: tuple) -> int:
     """Token stride of a bf16 ``[n][heads][d]`` tensor with dense rows."""
-    if x.dtype != torch.bfloat16:
+    if x.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be bfloat16")
-    if x.shape[1:] != (heads, d) or x.stride(2) != 1 or (heads > 1 and x.stride(1) != d):
-        raise ValueError(f"{name} must be [n_tokens][{heads}][{d}] with dense rows")
-    return x.stride(0) if x.shape[0] > 1 else 0
+    n, heads, d = shape
+    st = x.stride()
+    if x.shape != shape or st[2] != 1 or (st[1] != d and heads > 1):
+        raise ValueError(f"{name} must be {shape} with dense rows")
+    return st[0] if n > 1 else 0
 
 
 def loopvq_append(cfg: LoopVQConfig, layer: int, loop_step: int, q: torch.Tensor | None,
@@ -277,49 +292,36 @@ def loopvq_append(cfg: LoopVQConfig, layer: int, loop_step: int, q: torch.Tensor
     slot_mapping int64 ``[n]``, written (with block_table) when given."""
     n, batch = k.shape[0], seq_lens.shape[0]
     hq, hkv, d = cfg.n_q_heads, cfg.n_kv_heads, cfg.head_dim
-    qs = 0
+    bf16, int32 = torch.bfloat16, torch.int32
+    q_ptr = qo_ptr = rope_ptr = starts_ptr = table_ptr = slots_ptr = None
+    qs = positions = rot = 0
     if q is not None:
-        qs = _token_rows("q", q, hq, d)
-        if q.shape[0] != n:
-            raise ValueError("q and k must have the same number of tokens")
-        if q_out is None or q_out.dtype != torch.bfloat16 or q_out.shape != q.shape or \
-                not q_out.is_contiguous():
-            raise ValueError("q_out must be dense bfloat16 of q's shape")
-    ks, vs = _token_rows("k", k, hkv, d), _token_rows("v", v, hkv, d)
-    if v.shape[0] != n:
-        raise ValueError("k and v must have the same number of tokens")
-    slots = cfg.prefix_tokens + cfg.recent_tokens
-    for name, w in (("win_k", win_k), ("win_v", win_v)):
-        if w.dtype != torch.bfloat16 or w.shape != (batch, hkv, slots, d) or not w.is_contiguous():
-            raise ValueError(f"{name} must be dense bfloat16 [B][Hkv][P+R][d]")
-    if evicted.dtype != torch.bfloat16 or not evicted.is_contiguous() or evicted.numel() != \
-            cfg.n_layers * cfg.n_loops * 2 * n * hkv * d:
-        raise ValueError("evicted must be dense bfloat16 [L][G][2][g][n_tokens][Hkv][d]")
-    positions = rot = 0
+        if q_out is None:
+            raise ValueError("q needs q_out")
+        qs = _token_rows("q", q, (n, hq, d))
+        q_ptr, qo_ptr = q.data_ptr(), _dense("q_out", q_out, bf16, (n, hq, d))
+    ks, vs = _token_rows("k", k, (n, hkv, d)), _token_rows("v", v, (n, hkv, d))
+    window = (batch, hkv, cfg.prefix_tokens + cfg.recent_tokens, d)
+    wk_ptr, wv_ptr = _dense("win_k", win_k, bf16, window), _dense("win_v", win_v, bf16, window)
+    g = cfg.loop_group
+    ev_ptr = _dense("evicted", evicted, bf16, (cfg.n_layers, cfg.n_loops // g, 2, g, n, hkv, d))
     if rope is not None:
-        if rope.dtype != torch.float32 or rope.dim() != 2 or not rope.is_contiguous():
-            raise ValueError("rope must be dense float32 [positions][rot_dim]")
         positions, rot = rope.shape
-    if seq_lens.dtype != torch.int32 or not seq_lens.is_contiguous():
-        raise ValueError("seq_lens must be dense int32 [B]")
-    if token_starts is not None and (token_starts.dtype != torch.int32 or
-                                     not token_starts.is_contiguous() or
-                                     token_starts.shape[0] != batch + 1):
-        raise ValueError("token_starts must be dense int32 [B + 1]")
+        rope_ptr = _dense("rope", rope, torch.float32, (positions, rot))
+    lens_ptr = _dense("seq_lens", seq_lens, int32, (batch,))
+    if token_starts is not None:
+        starts_ptr = _dense("token_starts", token_starts, int32, (batch + 1,))
     if slot_mapping is not None:
-        if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (n,) or \
-                not slot_mapping.is_contiguous():
-            raise ValueError("slot_mapping must be dense int64 [n_tokens]")
-        if block_table is None or block_table.dtype != torch.int32 or \
-                block_table.shape != (batch, cfg.max_pages_per_seq) or not block_table.is_contiguous():
-            raise ValueError("block_table must be dense int32 [B][max_pages_per_seq]")
+        slots_ptr = _dense("slot_mapping", slot_mapping, torch.int64, (n,))
+        if block_table is None:
+            raise ValueError("slot_mapping needs block_table")
+        table_ptr = _dense("block_table", block_table, int32, (batch, cfg.max_pages_per_seq))
     _on_current_device("loopvq_append", q, k, v, rope, seq_lens, win_k, win_v, q_out, evicted,
                        token_starts, block_table, slot_mapping)
     st = _lib.loopvq_append(
-        cfg.c_ref(), layer, loop_step, batch, n, _ptr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs,
-        _ptr(rope), positions, rot, int(interleaved), _ptr(token_starts), seq_lens.data_ptr(),
-        _ptr(block_table) if slot_mapping is not None else None, win_k.data_ptr(), win_v.data_ptr(),
-        _ptr(q_out) if q is not None else None, evicted.data_ptr(), _ptr(slot_mapping), _stream(stream))
+        cfg.c_ref(), layer, loop_step, batch, n, q_ptr, qs, k.data_ptr(), ks, v.data_ptr(), vs,
+        rope_ptr, positions, rot, interleaved, starts_ptr, lens_ptr, table_ptr, wk_ptr, wv_ptr, qo_ptr,
+        ev_ptr, slots_ptr, _stream(stream))
     _check("loopvq_append", st)
 
 
