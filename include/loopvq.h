@@ -90,7 +90,11 @@ enum {
   LOOPVQ_DECODE_STATUS_TIMEOUT = 8,
   /* with LOOPVQ_DECODE_STATUS_TIMEOUT: the work in flight could not be
    * waited for before the kernel exited */
-  LOOPVQ_DECODE_STATUS_UNDRAINED = 16
+  LOOPVQ_DECODE_STATUS_UNDRAINED = 16,
+  /* loopvq_decode_attn_shared: group_starts that do not ascend inside
+   * [0, batch], a group of more than max_group sequences, or more shared or own
+   * tokens than the call's bounds; what lies past a bound was left out */
+  LOOPVQ_DECODE_STATUS_BAD_GROUP = 32
 };
 
 /*
@@ -445,6 +449,48 @@ loopvq_status loopvq_prefill_attn(const loopvq_config* cfg, int layer, int loop_
                                   const void* win_k, const void* win_v, float sm_scale,
                                   int out_dtype, void* out, float* lse, void* workspace,
                                   size_t workspace_bytes, void* stream);
+
+/*
+ * Decode attention of a batch whose sequences share quantised prefixes
+ * (parallel samples of one prompt, requests behind one system prompt): what
+ * loopvq_decode_attn computes, with the tokens that a group of sequences has
+ * in common read and dequantised once for the whole group.
+ *
+ * Group i is the sequences group_starts[i] .. group_starts[i+1]-1. Their
+ * first shared_lens[i] quantised tokens are the same: where their page tables
+ * reach those tokens, the pages hold the same indices (usually they are the
+ * same pages; a page that the prefix ends in may be each sequence's own copy).
+ * The call reads them through the first sequence's row of block_table, which
+ * names the pages of all shared_lens[i] tokens whatever its own length. The
+ * remaining quantised tokens are read through each sequence's own row, the
+ * bf16 windows from each sequence's own slots. A sequence in no group shares
+ * nothing; one with fewer quantised tokens than shared_lens[i] uses the first
+ * of them.
+ *
+ *  group_starts  int32 [n_groups + 1], ascending, in [0, batch].
+ *  shared_lens   int32 [n_groups], shared quantised tokens of each group.
+ *  max_group, max_shared_len, max_own_len
+ *                bounds on the host: sequences of a group, shared quantised
+ *                tokens of a group, and quantised tokens of a sequence past the
+ *                shared ones. Device values past a bound are clipped to it and
+ *                set LOOPVQ_DECODE_STATUS_BAD_GROUP.
+ *  workspace     at least loopvq_decode_shared_workspace_bytes(cfg, batch,
+ *                n_groups, max_group, max_shared_len, max_own_len) bytes,
+ *                16-byte aligned; the status word as for loopvq_decode_attn.
+ *                Calls that may overlap need workspaces of their own.
+ * Every other argument as for loopvq_decode_attn.
+ */
+size_t loopvq_decode_shared_workspace_bytes(const loopvq_config* cfg, int batch, int n_groups,
+                                            int max_group, int max_shared_len, int max_own_len);
+loopvq_status loopvq_decode_attn_shared(const loopvq_config* cfg, int layer, int loop_step,
+                                        int batch, int n_groups, int max_group,
+                                        int max_shared_len, int max_own_len, const void* q,
+                                        const uint8_t* pool, const float* codebooks,
+                                        const int32_t* block_table, const int32_t* seq_lens,
+                                        const int32_t* group_starts, const int32_t* shared_lens,
+                                        const void* win_k, const void* win_v, float sm_scale,
+                                        int out_dtype, void* out, float* lse, void* workspace,
+                                        size_t workspace_bytes, void* stream);
 
 /*
  * Decode attention that needs no workspace from the caller. The pages have

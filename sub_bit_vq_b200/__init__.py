@@ -5,6 +5,7 @@ loads it and marshals arguments. Importing it without the built library
 raises ``ImportError``: there is no CPU fallback.
 """
 from .binding import (  # noqa: F401
+    LOOPVQ_DECODE_STATUS_BAD_GROUP,
     LOOPVQ_DECODE_STATUS_BAD_PAGE,
     LOOPVQ_ENCODE_STATUS_TIMEOUT,
     LOOPVQ_ENCODE_STATUS_UNDRAINED,
@@ -25,6 +26,8 @@ from .binding import (  # noqa: F401
     loopvq_cache_layout,
     loopvq_decode_attn,
     loopvq_decode_attn_noalloc,
+    loopvq_decode_attn_shared,
+    loopvq_decode_shared_workspace_bytes,
     loopvq_decode_workspace_bytes,
     loopvq_encode,
     loopvq_encode_evict,

@@ -36,6 +36,7 @@ LOOPVQ_DECODE_STATUS_SHARED_BASE = 2
 LOOPVQ_DECODE_STATUS_RANGE = 4
 LOOPVQ_DECODE_STATUS_TIMEOUT = 8
 LOOPVQ_DECODE_STATUS_UNDRAINED = 16
+LOOPVQ_DECODE_STATUS_BAD_GROUP = 32
 
 
 class LoopVQError(RuntimeError):
@@ -101,6 +102,11 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.loopvq_decode_attn.restype = I
     lib.loopvq_decode_attn.argtypes = [cfgp, I, I, I, I, P, P, P, P, P, P, P, F, I, P, P, P, SZ,
                                        P]
+    lib.loopvq_decode_shared_workspace_bytes.restype = SZ
+    lib.loopvq_decode_shared_workspace_bytes.argtypes = [cfgp, I, I, I, I, I]
+    lib.loopvq_decode_attn_shared.restype = I
+    lib.loopvq_decode_attn_shared.argtypes = [cfgp, I, I, I, I, I, I, I, P, P, P, P, P, P, P, P, P, F,
+                                              I, P, P, P, SZ, P]
     lib.loopvq_decode_attn_noalloc.restype = I
     lib.loopvq_decode_attn_noalloc.argtypes = [cfgp, I, I, I, I, P, P, P, P, P, P, P, F, I, P, P, P]
     lib.loopvq_bf16_decode_workspace_bytes.restype = SZ
@@ -119,6 +125,7 @@ _lib = _load()
 EXPORTED = ("loopvq_status_string", "loopvq_cache_layout", "loopvq_encode", "loopvq_encode_evict",
             "loopvq_encode_status", "loopvq_append", "loopvq_prefill_workspace_bytes", "loopvq_prefill_attn",
             "loopvq_decode_workspace_bytes", "loopvq_decode_attn", "loopvq_decode_attn_noalloc",
+            "loopvq_decode_shared_workspace_bytes", "loopvq_decode_attn_shared",
             "loopvq_bf16_decode_workspace_bytes", "loopvq_bf16_decode_attn",
             "loopvq_kmeans_assign_bytes", "loopvq_kmeans_step")
 
@@ -433,6 +440,54 @@ def loopvq_decode_attn_noalloc(cfg: LoopVQConfig, layer: int, loop_step: int, q:
         _ptr(block_table), _ptr(seq_lens), _ptr(win_k), _ptr(win_v), float(sm_scale), odt,
         _ptr(out), _ptr(lse), _stream(stream))
     _check("loopvq_decode_attn_noalloc", st)
+
+
+def loopvq_decode_shared_workspace_bytes(cfg: LoopVQConfig, batch: int, n_groups: int, max_group: int,
+                                         max_shared_len: int, max_own_len: int) -> int:
+    return int(_lib.loopvq_decode_shared_workspace_bytes(cfg.c_ref(), batch, n_groups, max_group,
+                                                         max_shared_len, max_own_len))
+
+
+def loopvq_decode_attn_shared(cfg: LoopVQConfig, layer: int, loop_step: int, q: torch.Tensor,
+                              pool: torch.Tensor, codebooks: torch.Tensor,
+                              block_table: torch.Tensor, seq_lens: torch.Tensor,
+                              group_starts: torch.Tensor, shared_lens: torch.Tensor,
+                              win_k: torch.Tensor, win_v: torch.Tensor, out: torch.Tensor,
+                              workspace: torch.Tensor, max_group: int, max_shared_len: int,
+                              max_own_len: int, lse: torch.Tensor | None = None,
+                              sm_scale: float | None = None, stream=None) -> None:
+    """loopvq_decode_attn for groups of sequences that share their first
+    quantised tokens. group_starts int32 ``[n_groups + 1]``, shared_lens int32
+    ``[n_groups]``; max_group, max_shared_len and max_own_len bound a group's
+    sequences, its shared tokens and a sequence's further quantised tokens."""
+    batch, n_groups = q.shape[0], shared_lens.shape[0]
+    hq, hkv, d = cfg.n_q_heads, cfg.n_kv_heads, cfg.head_dim
+    if sm_scale is None:
+        sm_scale = d ** -0.5
+    bf16, int32 = torch.bfloat16, torch.int32
+    if out.dtype not in (torch.float32, bf16):
+        raise TypeError("out must be float32 or bfloat16")
+    odt = LOOPVQ_DTYPE_F32 if out.dtype is torch.float32 else LOOPVQ_DTYPE_BF16
+    rows = (batch, hq, d)
+    window = (batch, hkv, cfg.prefix_tokens + cfg.recent_tokens, d)
+    args = (_dense("q", q, bf16, rows), pool.data_ptr(), codebooks.data_ptr(),
+            _dense("block_table", block_table, int32, (batch, cfg.max_pages_per_seq)),
+            _dense("seq_lens", seq_lens, int32, (batch,)),
+            _dense("group_starts", group_starts, int32, (n_groups + 1,)),
+            _dense("shared_lens", shared_lens, int32, (n_groups,)),
+            _dense("win_k", win_k, bf16, window), _dense("win_v", win_v, bf16, window))
+    _dense("out", out, out.dtype, rows)
+    if pool.dtype is not torch.uint8 or codebooks.dtype is not torch.float32:
+        raise TypeError("pool must be uint8 and codebooks float32")
+    if lse is not None:
+        _dense("lse", lse, torch.float32, (batch, hq))
+    _on_current_device("loopvq_decode_attn_shared", q, pool, codebooks, block_table, seq_lens,
+                       group_starts, shared_lens, win_k, win_v, out, workspace, lse)
+    st = _lib.loopvq_decode_attn_shared(
+        cfg.c_ref(), layer, loop_step, batch, n_groups, max_group, max_shared_len, max_own_len, *args,
+        sm_scale, odt, out.data_ptr(), _ptr(lse), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream(stream))
+    _check("loopvq_decode_attn_shared", st)
 
 
 def loopvq_bf16_decode_workspace_bytes(batch: int, n_q_heads: int, head_dim: int,

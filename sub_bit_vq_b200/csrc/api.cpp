@@ -3,6 +3,7 @@
 
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <climits>
 #include <cstring>
@@ -346,6 +347,21 @@ loopvq_status decode_common(const loopvq_config* cfg, int layer, int loop_step, 
   return launch_decode(a);
 }
 
+// Longest sequence of a shared-prefix call with these bounds.
+int shared_max_seq_len(const Geometry& g, int max_shared_len, int max_own_len) {
+  const int64_t vq = std::min(static_cast<int64_t>(max_shared_len) + max_own_len,
+                              static_cast<int64_t>(g.max_pages_per_seq) * g.Pg);
+  return static_cast<int>(std::min<int64_t>(g.W + vq, INT_MAX));
+}
+
+bool shared_bounds_ok(const Geometry& g, int batch, int n_groups, int max_group, int max_shared_len,
+                      int max_own_len) {
+  const int64_t most = static_cast<int64_t>(g.max_pages_per_seq) * g.Pg;
+  return batch > 0 && batch <= g.max_batch && n_groups >= 0 && n_groups <= batch && max_group >= 0 &&
+         max_group <= batch && (n_groups == 0 || max_group > 0) && max_shared_len >= 0 &&
+         max_shared_len <= most && max_own_len >= 0 && max_own_len <= most;
+}
+
 }  // namespace
 }  // namespace loopvq
 
@@ -380,6 +396,40 @@ loopvq_status loopvq_prefill_attn(const loopvq_config* cfg, int layer, int loop_
   return loopvq::decode_common(cfg, layer, loop_step, batch, n_queries, max_seq_len, q, pool,
                                codebooks, block_table, seq_lens, win_k, win_v, sm_scale, out_dtype,
                                out, lse, workspace, workspace_bytes, stream);
+}
+
+size_t loopvq_decode_shared_workspace_bytes(const loopvq_config* cfg, int batch, int n_groups,
+                                            int max_group, int max_shared_len, int max_own_len) {
+  Geometry g;
+  if (loopvq::make_geometry(cfg, &g) != LOOPVQ_OK ||
+      !loopvq::shared_bounds_ok(g, batch, n_groups, max_group, max_shared_len, max_own_len))
+    return 0;
+  return loopvq::decode_workspace_bytes(batch * g.Hq, g.J, g.d);
+}
+
+loopvq_status loopvq_decode_attn_shared(const loopvq_config* cfg, int layer, int loop_step,
+                                        int batch, int n_groups, int max_group,
+                                        int max_shared_len, int max_own_len, const void* q,
+                                        const uint8_t* pool, const float* codebooks,
+                                        const int32_t* block_table, const int32_t* seq_lens,
+                                        const int32_t* group_starts, const int32_t* shared_lens,
+                                        const void* win_k, const void* win_v, float sm_scale,
+                                        int out_dtype, void* out, float* lse, void* workspace,
+                                        size_t workspace_bytes, void* stream) {
+  Geometry g;
+  loopvq_status st = loopvq::make_geometry(cfg, &g);
+  if (st != LOOPVQ_OK) return st;
+  if (!loopvq::shared_bounds_ok(g, batch, n_groups, max_group, max_shared_len, max_own_len))
+    return LOOPVQ_ERR_INVALID_ARG;
+  if (n_groups > 0 && (group_starts == nullptr || shared_lens == nullptr)) return LOOPVQ_ERR_INVALID_ARG;
+  if (!loopvq::aligned(group_starts, 4) || !loopvq::aligned(shared_lens, 4)) return LOOPVQ_ERR_INVALID_ARG;
+  if (workspace_bytes < loopvq_decode_shared_workspace_bytes(cfg, batch, n_groups, max_group, max_shared_len,
+                                                             max_own_len))
+    return LOOPVQ_ERR_WORKSPACE;
+  return loopvq::decode_common(cfg, layer, loop_step, batch, 1,
+                               loopvq::shared_max_seq_len(g, max_shared_len, max_own_len), q, pool,
+                               codebooks, block_table, seq_lens, win_k, win_v, sm_scale, out_dtype, out,
+                               lse, workspace, workspace_bytes, stream);
 }
 
 size_t loopvq_bf16_decode_workspace_bytes(int batch, int n_q_heads, int head_dim,

@@ -44,6 +44,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "tcgen05.cuh"
 
 namespace loopvq {
 namespace {
@@ -93,10 +94,6 @@ struct PrefillParams {
   float scale_log2;
 };
 
-__device__ __forceinline__ uint32_t u32s(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-
 // Byte offset of element (r, k) of a K-major operand with KP columns
 // (8-row x 16-byte core matrices, K halves 128 bytes apart).
 template <int KP>
@@ -112,57 +109,6 @@ __device__ __forceinline__ uint64_t sdesc(uint32_t saddr, int kp) {
 // bf16 x bf16 -> fp32, K-major A and B, M = 128.
 __host__ __device__ constexpr uint32_t idesc_bf16(int n) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((static_cast<uint32_t>(n) >> 3) << 17) | ((128u >> 4) << 24);
-}
-
-__device__ __forceinline__ bool pf_wait(uint32_t bar, uint32_t parity, int spin) {
-  for (int it = 0; it < spin; ++it) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred P;\n mbarrier.try_wait.parity.shared::cta.b64 P, [%1], %2;\n"
-        " selp.u32 %0, 1, 0, P;\n}\n"
-        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-    if (ok != 0u) return true;
-  }
-  return false;
-}
-
-__device__ __forceinline__ void tld32(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
-      "%30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-}
-
-__device__ __forceinline__ void tst32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
-      "%30, %31, %32};"
-      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
-        "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
-        "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
-        "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
-
-__device__ __forceinline__ void mma_bf16(uint32_t tmem_d, uint64_t ad, uint64_t bd, uint32_t idesc,
-                                         uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n"
-      ::"r"(tmem_d), "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate) : "memory");
-}
-
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-               : "memory");
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -269,7 +215,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_tc_kernel(const Prefill
   const uint32_t tmem = *tmem_slot;
   const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
   const uint32_t my_s = lane_base + kTmemS + colh * 32, my_o = lane_base + kTmemO + colh * 64;
-  bool failed = !window && !pf_wait(bar_cb, 0, kPfSpin);
+  bool failed = !window && !mbar_wait(bar_cb, 0, kPfSpin);
   failed = __syncthreads_or(failed);
 
   const uint8_t* pool_h = p.pool_lg + hkv * p.pool_stride_head;
@@ -375,7 +321,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_tc_kernel(const Prefill
     }
     // the previous tile's O product has read Ps and Vs (and O may be rescaled)
     if (pending_o >= 0) {
-      const bool ok = pf_wait(bar_o, static_cast<uint32_t>(pending_o), kPfSpin);
+      const bool ok = mbar_wait(bar_o, static_cast<uint32_t>(pending_o), kPfSpin);
       if (__syncthreads_or(!ok)) {
         failed = true;
         break;
@@ -406,12 +352,12 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_tc_kernel(const Prefill
       for (int part = 0; part < 2; ++part)
 #pragma unroll
         for (int kk = 0; kk < kPfD / 16; ++kk)
-          mma_bf16(tmem + kTmemS, sdesc(qs_a + kk * 256, kPfD), sdesc(ks_a + part * kKsBytes + kk * 256, kPfD),
+          tc_mma_f16(tmem + kTmemS, sdesc(qs_a + kk * 256, kPfD), sdesc(ks_a + part * kKsBytes + kk * 256, kPfD),
                    idesc_bf16(kPfTok), (part > 0 || kk > 0) ? 1u : 0u);
-      mma_commit(bar_s);
+      tc_commit(bar_s);
     }
     {
-      const bool ok = pf_wait(bar_s, static_cast<uint32_t>(tile & 1), kPfSpin);
+      const bool ok = mbar_wait(bar_s, static_cast<uint32_t>(tile & 1), kPfSpin);
       if (__syncthreads_or(!ok)) {
         failed = true;
         pending_o = -2;                                // the S product may still write TMEM
@@ -475,9 +421,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_tc_kernel(const Prefill
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll
       for (int kk = 0; kk < kPfTok / 16; ++kk)
-        mma_bf16(tmem + kTmemO, sdesc(ps_a + kk * 256, kPfTok), sdesc(vs_a + kk * 256, kPfTok),
+        tc_mma_f16(tmem + kTmemO, sdesc(ps_a + kk * 256, kPfTok), sdesc(vs_a + kk * 256, kPfTok),
                  idesc_bf16(kPfD), (o_live || kk > 0) ? 1u : 0u);
-      mma_commit(bar_o);
+      tc_commit(bar_o);
     }
     o_live = true;
     pending_o = tile & 1;
@@ -486,7 +432,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_tc_kernel(const Prefill
 
   // ---- the record (m, l, o) of every row ------------------------------------------------
   if (!failed && pending_o >= 0) {
-    const bool ok = pf_wait(bar_o, static_cast<uint32_t>(pending_o), kPfSpin);
+    const bool ok = mbar_wait(bar_o, static_cast<uint32_t>(pending_o), kPfSpin);
     failed = __syncthreads_or(!ok);
     if (!failed) pending_o = -1;
   }
@@ -515,9 +461,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_tc_kernel(const Prefill
     // may still write, flag the status word, poison the record
     if (tid == 0) {
       bool drained = true;
-      if (pending_o >= 0) drained = pf_wait(bar_o, static_cast<uint32_t>(pending_o), kPfDrainSpin) && drained;
-      if (pending_o == -2) drained = pf_wait(bar_s, static_cast<uint32_t>(n_tiles_done & 1), kPfDrainSpin) && drained;
-      if (!window) drained = pf_wait(bar_cb, 0, kPfDrainSpin) && drained;
+      if (pending_o >= 0) drained = mbar_wait(bar_o, static_cast<uint32_t>(pending_o), kPfDrainSpin) && drained;
+      if (pending_o == -2) drained = mbar_wait(bar_s, static_cast<uint32_t>(n_tiles_done & 1), kPfDrainSpin) && drained;
+      if (!window) drained = mbar_wait(bar_cb, 0, kPfDrainSpin) && drained;
       if (p.status != nullptr) atomicOr(p.status, drained ? LOOPVQ_DECODE_STATUS_TIMEOUT
                                                           : (LOOPVQ_DECODE_STATUS_TIMEOUT | LOOPVQ_DECODE_STATUS_UNDRAINED));
     }
