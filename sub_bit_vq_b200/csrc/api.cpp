@@ -301,14 +301,14 @@ loopvq_status loopvq_kmeans_step(const loopvq_config* cfg, int layer, int loop_g
 namespace loopvq {
 namespace {
 
-// Checks and launches a decode of n_queries queries per sequence (decode:
-// 1; prefill over the cache: a chunk of queries).
-loopvq_status decode_common(const loopvq_config* cfg, int layer, int loop_step, int batch,
-                            int n_queries, int max_seq_len, const void* q, const uint8_t* pool,
-                            const float* codebooks, const int32_t* block_table,
-                            const int32_t* seq_lens, const void* win_k, const void* win_v,
-                            float sm_scale, int out_dtype, void* out, float* lse, void* workspace,
-                            size_t workspace_bytes, void* stream) {
+// Checks a decode of n_queries queries per sequence (decode: 1; prefill
+// over the cache: a chunk of queries) and fills its geometry.
+loopvq_status decode_check(const loopvq_config* cfg, int layer, int loop_step, int batch,
+                           int n_queries, int max_seq_len, const void* q, const uint8_t* pool,
+                           const float* codebooks, const int32_t* block_table,
+                           const int32_t* seq_lens, const void* win_k, const void* win_v,
+                           float sm_scale, int out_dtype, void* out, float* lse, void* workspace,
+                           size_t workspace_bytes, Geometry* geo) {
   Geometry g;
   loopvq_status st = make_geometry(cfg, &g);
   if (st != LOOPVQ_OK) return st;
@@ -330,6 +330,23 @@ loopvq_status decode_common(const loopvq_config* cfg, int layer, int loop_step, 
   if (pages > g.max_pages_per_seq) return LOOPVQ_ERR_INVALID_ARG;
   const size_t need = decode_workspace_bytes(batch * n_queries * g.Hq, g.J, g.d);
   if (workspace_bytes < need) return LOOPVQ_ERR_WORKSPACE;
+  *geo = g;
+  return LOOPVQ_OK;
+}
+
+// Checks and launches it.
+loopvq_status decode_common(const loopvq_config* cfg, int layer, int loop_step, int batch,
+                            int n_queries, int max_seq_len, const void* q, const uint8_t* pool,
+                            const float* codebooks, const int32_t* block_table,
+                            const int32_t* seq_lens, const void* win_k, const void* win_v,
+                            float sm_scale, int out_dtype, void* out, float* lse, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  Geometry g;
+  loopvq_status st = decode_check(cfg, layer, loop_step, batch, n_queries, max_seq_len, q, pool, codebooks,
+                                  block_table, seq_lens, win_k, win_v, sm_scale, out_dtype, out, lse,
+                                  workspace, workspace_bytes, &g);
+  if (st != LOOPVQ_OK) return st;
+  const int pages = pages_for(g, max_seq_len);
   loopvq_status err = LOOPVQ_OK;
   const int sms = current_sm_count(&err);
   if (err != LOOPVQ_OK) return err;
@@ -404,7 +421,9 @@ size_t loopvq_decode_shared_workspace_bytes(const loopvq_config* cfg, int batch,
   if (loopvq::make_geometry(cfg, &g) != LOOPVQ_OK ||
       !loopvq::shared_bounds_ok(g, batch, n_groups, max_group, max_shared_len, max_own_len))
     return 0;
-  return loopvq::decode_workspace_bytes(batch * g.Hq, g.J, g.d);
+  // enough for either form, so that the size does not depend on the output type
+  return std::max(loopvq::decode_workspace_bytes(batch * g.Hq, g.J, g.d),
+                  loopvq::shared_attn_workspace_bytes(g, batch, n_groups, max_group, max_shared_len, max_own_len));
 }
 
 loopvq_status loopvq_decode_attn_shared(const loopvq_config* cfg, int layer, int loop_step,
@@ -426,8 +445,19 @@ loopvq_status loopvq_decode_attn_shared(const loopvq_config* cfg, int layer, int
   if (workspace_bytes < loopvq_decode_shared_workspace_bytes(cfg, batch, n_groups, max_group, max_shared_len,
                                                              max_own_len))
     return LOOPVQ_ERR_WORKSPACE;
-  return loopvq::decode_common(cfg, layer, loop_step, batch, 1,
-                               loopvq::shared_max_seq_len(g, max_shared_len, max_own_len), q, pool,
+  const int max_seq_len = loopvq::shared_max_seq_len(g, max_shared_len, max_own_len);
+  if (loopvq::shared_attn_supported(g, n_groups, out_dtype)) {
+    st = loopvq::decode_check(cfg, layer, loop_step, batch, 1, max_seq_len, q, pool, codebooks, block_table,
+                              seq_lens, win_k, win_v, sm_scale, out_dtype, out, lse, workspace,
+                              workspace_bytes, &g);
+    if (st != LOOPVQ_OK) return st;
+    loopvq::SharedArgs a{&g,        layer,       loop_step, batch,        n_groups,    max_group, max_shared_len,
+                         max_own_len, q,         pool,      codebooks,    block_table, seq_lens,  group_starts,
+                         shared_lens, win_k,     win_v,     sm_scale,     out,         lse,       workspace,
+                         stream};
+    return loopvq::launch_shared_attn(a);
+  }
+  return loopvq::decode_common(cfg, layer, loop_step, batch, 1, max_seq_len, q, pool,
                                codebooks, block_table, seq_lens, win_k, win_v, sm_scale, out_dtype, out,
                                lse, workspace, workspace_bytes, stream);
 }

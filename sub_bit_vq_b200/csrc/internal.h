@@ -75,6 +75,31 @@ size_t prefill_tc_workspace_bytes(const Geometry& g, int batch, int n_queries, i
                                   int* CH);
 loopvq_status launch_prefill_tc(const DecodeArgs& a, size_t workspace_bytes);
 
+// Decode attention of groups that share a quantised prefix on the tensor
+// cores (shared_attn.cu): bf16 outputs, head_dim a multiple of 16 up to 128.
+struct SharedArgs {
+  const Geometry* geo;
+  int layer, loop_step, batch, n_groups, max_group, max_shared, max_own;
+  const void* q;
+  const uint8_t* pool;
+  const float* codebooks;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* group_starts;
+  const int32_t* shared_lens;
+  const void* win_k;
+  const void* win_v;
+  float sm_scale;
+  void* out;
+  float* lse;
+  void* workspace;
+  void* stream;
+};
+bool shared_attn_supported(const Geometry& g, int n_groups, int out_dtype);
+size_t shared_attn_workspace_bytes(const Geometry& g, int batch, int n_groups, int max_group, int max_shared,
+                                   int max_own);
+loopvq_status launch_shared_attn(const SharedArgs& a);
+
 struct EncodeArgs {
   const Geometry* geo;
   int layer, gamma, kv, n_tokens;

@@ -1,0 +1,1287 @@
+// Decode attention for groups of sequences that share a quantised prefix, on
+// the tensor cores (sm_100a).
+//
+// One query per sequence leaves a decode step without a matrix product, but a
+// group of sequences over the same tokens is one: with the group's queries as
+// the rows of Q,
+//   S^T = K Q^T       (M = 128 token rows,  N = query rows, K = d)
+//   O^T += V^T P      (M = 128 channels,    N = query rows, K = 128 tokens)
+// The tokens (then the channels) are the M side, so the products cost what the
+// group's rows need (N = 16, 32 or 64) and not a 128-row tile.
+//
+// Three parts of one grid and one merge:
+//   shared blocks  (group, kv-head, row tile, split of the shared tokens): the
+//                  tensor-core pipeline below, one record (m, l, o[d]) per row.
+//   own blocks     (kv-head, part): one warp per (sequence, query head, chunk
+//                  of its own quantised tokens), scored against the same
+//                  codebooks in shared memory, lane = channel group; chunk 0
+//                  takes the bf16 window too. One record per chunk.
+//   merge kernel   log-sum-exp join of a pair's records.
+//
+// Codewords are dequantised from fp16 tables in shared memory, [E] rows of 256
+// bytes holding entry (e, j) at byte j*2c: a lane that reads channel group j
+// hits banks that depend on j only, and in the pool's rotated rows lane = slot i
+// finds group (s + i) mod J at byte s, so the lookups of a half-warp never
+// collide. The tile rows are written in the 128-byte swizzle, where the same
+// rotation keeps the stores free of conflicts too. The value tile is the same
+// [token][channel] layout read as an M-major operand, so nothing is transposed.
+//
+// Shared pipeline, 17 warps: warps 8-15 dequantise (a tile is four index
+// blocks; warp w fills block w % 4, half of its groups), warp 16 issues the
+// products, warps 0-7 turn S^T into P (warp w reads TMEM lanes 32 (w % 4) ..,
+// the column half w / 4). K has one buffer, V one per half tile, S^T two, P one;
+// mbarriers hand them over, so the dequantisation of tile i + 1 runs under the
+// softmax of tile i.
+//
+// Softmax: per row a reference m, raised only when a score passes it by more
+// than kRaise (then to the tile's maximum - kTop), so P = 2^(x - m) stays below
+// 2^kRaise and keeps fp16's full precision down to 2^-20 of the maximum; sums
+// are float32 over unrounded weights.
+//
+// Rounding. Keys, values and weights enter the products as fp16: half a step is
+// 2^-11 of each value, an eighth of the bf16 output's own. Codebooks and queries
+// are scaled by powers of two into fp16's range (exact), so their magnitude does
+// not matter. float32 outputs take the streaming kernels.
+
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include <atomic>
+#include <climits>
+#include <type_traits>
+
+#include "common.cuh"
+#include "internal.h"
+#include "tcgen05.cuh"
+
+namespace loopvq {
+namespace {
+
+constexpr int kShWarps = 17;
+constexpr int kShThreads = kShWarps * 32;
+constexpr int kSoftWarps = 8;
+constexpr int kDeqWarps = 8;
+constexpr int kMmaWarp = 16;
+constexpr int kTileRows = 128;            // token rows of a tile (4 index blocks of up to 32 slots)
+constexpr int kMaxRows = 64;              // query rows of a block
+constexpr float kRaise = 14.f;            // log2: a weight reaches 2^14 at most
+constexpr float kTop = 6.f;               // log2: weight of the maximum after a raise
+constexpr float kUnset = -1e30f;          // reference of a row that has seen no token
+#ifndef LOOPVQ_TC_SPIN
+#define LOOPVQ_TC_SPIN (1 << 20)
+#endif
+constexpr int kShSpin = LOOPVQ_TC_SPIN;
+constexpr int kShDrainSpin = 1 << 24;
+
+// Shared memory: bytes from the start of the dynamic allocation, which has to
+// be window address kShBase (the block's reserved shared memory ends there; the
+// host checks it), so that tables and tiles are immediate offsets.
+constexpr uint32_t kShBase = 0x400u;
+constexpr int kTabBytes = kE * 256;                        // one fp16 codebook slice
+constexpr int kKtabOff = 0;
+constexpr int kVtabOff = kTabBytes;
+constexpr int kKtileOff = 2 * kTabBytes;                   // [16 row groups][2 channel blocks][8][128 B]
+constexpr int kTileBytes = kTileRows * 256;
+constexpr int kVtileOff = kKtileOff + kTileBytes;
+constexpr int kPOff = kVtileOff + kTileBytes;              // [128 tokens][128 B], up to 64 rows of fp16
+constexpr int kQOff = kPOff + kTileRows * 128;             // [2 channel blocks][N][128 B]
+constexpr int kQBytes = kMaxRows * 256;
+constexpr int kMOff = kQOff + kQBytes;                     // float [2][64]: references
+constexpr int kCmOff = kMOff + 2 * kMaxRows * 4;           // float [4][64]: column maxima, then sums
+constexpr int kLimOff = kCmOff + 4 * kMaxRows * 4;         // int [64]: a row's shared tokens
+constexpr int kNvOff = kLimOff + kMaxRows * 4;             // int [4 tiles][4 blocks]: valid slots
+constexpr int kRedOff = kNvOff + 64;                       // float [17]: block reduction
+constexpr int kBarOff = kRedOff + 96;                      // mbarriers
+constexpr int kTmemSlotOff = kBarOff + 96;
+constexpr int kShSmem = kTmemSlotOff + 16;
+static_assert(kShSmem <= 227 * 1024, "shared memory above 227 KB");
+
+enum { kBarK = 0, kBarS0, kBarS1, kBarP, kBarV0, kBarV1, kBarVfree0, kBarVfree1, kBarO, kBarDrain, kBars };
+
+constexpr uint32_t kTmCols = 256, kTmS = 0, kTmO = 128;    // TMEM columns: S^T twice 64, O^T 64
+
+struct SharedParams {
+  const uint16_t* q;              // bf16 [B][Hq][d]
+  const uint8_t* pool_lg;         // pool at (layer, gamma, head 0)
+  int64_t pool_stride_head, page_bytes, plane_bytes;
+  const float* cb_k;              // (layer, head 0, gamma, K, tau): [J][E][c]
+  const float* cb_v;
+  int64_t cb_stride_head;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* group_starts;
+  const int32_t* shared_lens;
+  const uint16_t* win_k;
+  const uint16_t* win_v;
+  float* srec;                    // [pairs][NS][4 + d] records of the shared blocks
+  float* orec;                    // [pairs][NC][4 + d] records of the own chunks
+  int* status;
+  void* out;
+  float* lse;
+  int B, n_groups, Hq, Hkv, ratio, W, Pg, n_pages, max_pages_per_seq;
+  int max_group, max_shared, max_own;
+  int NS, RT, NC, CH;             // splits, row tiles, own records (window, chunks), tokens of a chunk
+  int shared_blocks, own_parts;   // grid: shared blocks, then Hkv * own_parts own blocks
+  int bpp;                        // index blocks of a page
+  float scale_log2;
+};
+
+template <int J_, int C_>
+struct Shape {
+  static constexpr int J = J_, C = C_, D = J * C;
+  static constexpr int LB = (32 / J) * J;
+  static constexpr int GR = (J % 16 == 0) ? 16 : (J % 8 == 0) ? 8 : 4;
+  static constexpr int NW = J / 4;                     // index words of a slot
+  static constexpr int ENTRY = 2 * C;                  // bytes of an fp16 codeword
+  static constexpr int TOK = 4 * LB;                   // tokens of a tile
+  static constexpr int RS = 4 + D;                     // floats of a record
+  static constexpr int TPS = 32 / J;                   // tokens a warp takes side by side (own tokens)
+};
+
+// K-major or M-major operand in the 128-byte swizzle.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3fffu) | (static_cast<uint64_t>(lbo >> 4) << 16) |
+         (static_cast<uint64_t>(sbo >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+// f16 x f16 -> f32, M = 128; ta, tb: operand is M-major (N-major).
+__device__ __forceinline__ uint32_t idesc_f16(int n, uint32_t ta, uint32_t tb) {
+  return (1u << 4) | (ta << 15) | (tb << 16) | ((static_cast<uint32_t>(n) >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// Byte offset of (row, byte of the row) in a tile: groups of 8 rows, each two
+// channel blocks of 8 x 128 bytes, 16-byte pieces swizzled by the row.
+__device__ __forceinline__ uint32_t tile_off(int row, int byte) {
+  return static_cast<uint32_t>((row >> 3) * 2048 + (byte >> 7) * 1024 + (row & 7) * 128 +
+                               (((byte & 127) & ~15) ^ ((row & 7) << 4)) + (byte & 15));
+}
+
+template <int BYTES>
+struct Word {
+  uint32_t w[BYTES / 4];
+};
+// Shared word(s) at window address a + OFF.
+template <int BYTES, uint32_t OFF>
+__device__ __forceinline__ Word<BYTES> lds(uint32_t a) {
+  Word<BYTES> r;
+  if constexpr (BYTES == 16)
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4+%5];"
+                 : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]) : "r"(a), "n"(OFF));
+  else
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2+%3];" : "=r"(r.w[0]), "=r"(r.w[1]) : "r"(a), "n"(OFF));
+  return r;
+}
+template <int BYTES, uint32_t OFF>
+__device__ __forceinline__ void sts(uint32_t a, const Word<BYTES>& r) {
+  if constexpr (BYTES == 16)
+    asm volatile("st.shared.v4.b32 [%0+%5], {%1, %2, %3, %4};" ::"r"(a), "r"(r.w[0]), "r"(r.w[1]), "r"(r.w[2]),
+                 "r"(r.w[3]), "n"(OFF) : "memory");
+  else
+    asm volatile("st.shared.v2.b32 [%0+%3], {%1, %2};" ::"r"(a), "r"(r.w[0]), "r"(r.w[1]), "n"(OFF) : "memory");
+}
+
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 half2_floats(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+// NC columns of this warp's 32 TMEM lanes.
+template <int NC>
+__device__ __forceinline__ void tld(uint32_t a, uint32_t (&r)[NC]) {
+  if constexpr (NC == 32) {
+    tld32(a, r);
+  } else if constexpr (NC == 16) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+        "%12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(a));
+  } else {
+    static_assert(NC == 8, "8, 16 or 32 columns");
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(a));
+  }
+}
+__device__ __forceinline__ void tst8(uint32_t a, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(a), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]) : "memory");
+}
+__device__ __forceinline__ void tld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tst_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("barrier.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ bool named_or(int id, int threads, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %3, 0;\n barrier.red.or.pred q, %1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r) : "r"(id), "r"(threads), "r"(v ? 1u : 0u) : "memory");
+  return r != 0u;
+}
+__device__ __forceinline__ float redux_fmax(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// Power of two that brings values of magnitude `top` just below 2^14 (1 for 0
+// or no finite value).
+__device__ __forceinline__ int scale_exp(float top) {
+  if (!(top > 0.f)) return 0;
+  return max(-100, min(100, 13 - ilogbf(top)));
+}
+
+// Largest finite magnitude over the block (every thread calls it).
+__device__ __forceinline__ float block_max(float v, float* red, int tid) {
+  v = redux_fmax(v);
+  __syncthreads();
+  if ((tid & 31) == 0) red[tid >> 5] = v;
+  __syncthreads();
+  float m = 0.f;
+#pragma unroll
+  for (int w = 0; w < kShWarps; ++w) m = fmaxf(m, red[w]);
+  return m;
+}
+__device__ __forceinline__ float finite_abs(float v) {
+  const float a = fabsf(v);
+  return a < INFINITY ? a : 0.f;
+}
+
+// One codebook slice [J][E][C] (float32) into an fp16 table, entries scaled by
+// 2^k (returned). Every thread calls it; the caller synchronises.
+template <int J, int C, int TAB>
+__device__ int load_table(const float* cb, float* red, int tid) {
+  constexpr int N = kE * J;                                // entries
+  constexpr int PER = (N + kShThreads - 1) / kShThreads;
+  constexpr int F4 = C / 4;
+  float4 v[PER][F4];
+  auto entry = [&](int k, int& e, int& j) {                // thread's k-th entry: 16 groups x 2 codewords a warp
+    const int f = tid + k * kShThreads;
+    if constexpr (J % 16 == 0) {
+      const int w = f >> 5, l = f & 31;
+      j = (w % (J / 16)) * 16 + (l & 15);
+      e = (w / (J / 16)) * 2 + (l >> 4);
+    } else {
+      e = f / J;
+      j = f - e * J;
+    }
+    return f < N;
+  };
+  float top = 0.f;
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    int e, j;
+    if (entry(k, e, j)) {
+#pragma unroll
+      for (int i = 0; i < F4; ++i) {
+        v[k][i] = __ldg(reinterpret_cast<const float4*>(cb + (static_cast<size_t>(j) * kE + e) * C) + i);
+        top = fmaxf(fmaxf(top, fmaxf(finite_abs(v[k][i].x), finite_abs(v[k][i].y))),
+                    fmaxf(finite_abs(v[k][i].z), finite_abs(v[k][i].w)));
+      }
+    }
+  }
+  const int ex = scale_exp(block_max(top, red, tid));
+  const float f = ldexpf(1.f, ex);
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    int e, j;
+    if (entry(k, e, j)) {
+      Word<2 * C> w;
+#pragma unroll
+      for (int i = 0; i < F4; ++i) {
+        w.w[2 * i] = half2_bits(v[k][i].x * f, v[k][i].y * f);
+        w.w[2 * i + 1] = half2_bits(v[k][i].z * f, v[k][i].w * f);
+      }
+      sts<2 * C, kShBase + TAB>(e * 256 + j * 2 * C, w);
+    }
+  }
+  return ex;
+}
+
+// Quantised tokens of sequence b.
+__device__ __forceinline__ int seq_vq(const SharedParams& p, int b) {
+  return max(0, min(__ldg(p.seq_lens + b) - p.W, p.max_pages_per_seq * p.Pg));
+}
+
+// Group of sequence b (-1: none); every lane of the warp calls it.
+__device__ __forceinline__ int group_of(const SharedParams& p, int b, int lane) {
+  int n = 0;
+  for (int i = lane; i < p.n_groups; i += 32) n += __ldg(p.group_starts + 1 + i) <= b ? 1 : 0;
+  const int g = __reduce_add_sync(0xffffffffu, n);
+  if (g >= p.n_groups || b < __ldg(p.group_starts + g) || b >= __ldg(p.group_starts + g + 1)) return -1;
+  if (b - __ldg(p.group_starts + g) >= p.max_group) return -1;
+  return g;
+}
+__device__ __forceinline__ int group_shared(const SharedParams& p, int g) {
+  return max(0, min(__ldg(p.shared_lens + g), p.max_shared));
+}
+
+// Number of shared tiles of split s of T tiles over NS splits: [first, last).
+__device__ __forceinline__ int split_tile(int T, int s, int NS) { return static_cast<int>(static_cast<int64_t>(T) * s / NS); }
+
+// Dequantises this lane's slot of a block: the w_n (up to W0) index words iw of
+// its row select entries of the table TAB, stored to its row of the tile TILE
+// at the places `at` gives (zeros for a slot at or past nv).
+template <int J, int C, int TAB, int TILE, int W0>
+__device__ __forceinline__ void fill_block(const uint32_t (&iw)[W0], const uint32_t (&at)[4 * W0], int w_n, int nv,
+                                           int lane) {
+  constexpr int ENTRY = Shape<J, C>::ENTRY, LB = Shape<J, C>::LB;
+  const bool whole = nv >= LB;                             // warp-uniform
+#pragma unroll
+  for (int w = 0; w < W0; ++w) {
+    if (w < w_n) {                                         // warp-uniform
+      Word<ENTRY> e[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)                          // codeword row (byte 1) | entry (byte 0)
+        e[i] = lds<ENTRY, kShBase + TAB>(__byte_perm(iw[w], at[4 * w + i], 0x5504u | (static_cast<uint32_t>(i) << 4)));
+      if (!whole && lane >= nv) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int k = 0; k < ENTRY / 4; ++k) e[i].w[k] = 0u;
+      }
+      if (lane < LB) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sts<ENTRY, kShBase + TILE>(at[4 * w + i] >> 16, e[i]);
+      }
+    }
+  }
+}
+
+// ---- shared blocks ---------------------------------------------------------------
+
+template <int J, int C, int N>
+__device__ void shared_block(const SharedParams& p, unsigned char* sm, int unit) {
+  using T = Shape<J, C>;
+  constexpr int D = T::D, NC = N / 2;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  float* m_ref = reinterpret_cast<float*>(sm + kMOff);
+  float* cm = reinterpret_cast<float*>(sm + kCmOff);
+  int* lim = reinterpret_cast<int*>(sm + kLimOff);
+  volatile int* nvs = reinterpret_cast<volatile int*>(sm + kNvOff);
+  float* red = reinterpret_cast<float*>(sm + kRedOff);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kTmemSlotOff);
+  auto bar = [&](int i) { return u32s(sm + kBarOff) + 8u * i; };
+
+  // unit = ((group * RT + row tile) * Hkv + head) * NS + split
+  const int split = unit % p.NS;
+  int x = unit / p.NS;
+  const int hkv = x % p.Hkv;
+  x /= p.Hkv;
+  const int rt = x % p.RT, g = x / p.RT;
+  const int lo = max(0, __ldg(p.group_starts + g)), hi = min(p.B, __ldg(p.group_starts + g + 1));
+  if (split == 0 && hkv == 0 && rt == 0 && tid == 0 && p.status != nullptr) {
+    const int a = __ldg(p.group_starts + g), z = __ldg(p.group_starts + g + 1), s = __ldg(p.shared_lens + g);
+    if (a < 0 || z > p.B || z < a || z - a > p.max_group || s < 0 || s > p.max_shared)
+      atomicOr(p.status, LOOPVQ_DECODE_STATUS_BAD_GROUP);
+  }
+  const int rows = min(max(0, min(hi - lo, p.max_group) * p.ratio - rt * N), N);   // this tile's query rows
+  const int S = group_shared(p, g);
+  const int tiles = (S + T::TOK - 1) / T::TOK;
+  const int tile0 = split_tile(tiles, split, p.NS), nt = split_tile(tiles, split + 1, p.NS) - tile0;
+  auto pair_of = [&](int c) {                              // (sequence, query head) of row c
+    const int r = rt * N + c;
+    return static_cast<int64_t>(lo + r / p.ratio) * p.Hq + hkv * p.ratio + r % p.ratio;
+  };
+  if (rows <= 0) return;                                   // block-uniform
+  if (nt <= 0) {
+    for (int c = tid; c < rows; c += kShThreads) {
+      float* rec = p.srec + (pair_of(c) * p.NS + split) * T::RS;
+      rec[0] = -INFINITY;
+      rec[1] = 0.f;
+    }
+    return;
+  }
+
+  // ---- setup: barriers, TMEM, tables, queries -----------------------------------
+  if (tid == 0) {
+    for (int i = 0; i < kBars; ++i) {
+      const uint32_t n = i == kBarK ? kDeqWarps : i == kBarP ? kSoftWarps : (i == kBarV0 || i == kBarV1) ? kDeqWarps / 2 : 1;
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar(i)), "r"(n) : "memory");
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(u32s(tmem_slot)),
+                 "r"(kTmCols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  const int kk = load_table<J, C, kKtabOff>(p.cb_k + hkv * p.cb_stride_head, red, tid);
+  const int kv = load_table<J, C, kVtabOff>(p.cb_v + hkv * p.cb_stride_head, red, tid);
+  // the queries, scaled into fp16: piece = 8 channels of a row
+  int kq;
+  {
+    constexpr int PIECES = N * D / 8, PER = (PIECES + kShThreads - 1) / kShThreads;
+    uint4 v[PER];
+    float top = 0.f;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int f = tid + k * kShThreads, c = f / (D / 8), part = f % (D / 8);
+      v[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (f < PIECES && c < rows) v[k] = *(reinterpret_cast<const uint4*>(p.q + pair_of(c) * D) + part);
+      const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 a = bf16x2_to_float2(w[i]);
+        top = fmaxf(top, fmaxf(finite_abs(a.x), finite_abs(a.y)));
+      }
+    }
+    kq = scale_exp(block_max(top, red, tid));
+    const float f2 = ldexpf(1.f, kq);
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int f = tid + k * kShThreads, c = f / (D / 8), byte = (f % (D / 8)) * 16;
+      if (f >= PIECES) continue;
+      const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+      uint32_t h[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 a = bf16x2_to_float2(w[i]);
+        h[i] = half2_bits(a.x * f2, a.y * f2);
+      }
+      *reinterpret_cast<uint4*>(sm + kQOff + (byte >> 7) * (N * 128) + c * 128 + ((byte & 127) ^ ((c & 7) << 4))) =
+          make_uint4(h[0], h[1], h[2], h[3]);
+    }
+  }
+  const float scale = ldexpf(p.scale_log2, -kk - kq);
+  // a row's shared tokens, its unset reference, zero value rows past a block's slots
+  for (int c = tid; c < N; c += kShThreads) {
+    lim[c] = c < rows ? min(S, seq_vq(p, static_cast<int>(pair_of(c) / p.Hq))) : INT_MAX;
+    m_ref[c] = m_ref[kMaxRows + c] = kUnset;
+  }
+  if constexpr (T::LB < 32) {
+    for (int i = tid; i < kTileBytes / 16; i += kShThreads)
+      *reinterpret_cast<uint4*>(sm + kVtileOff + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  proxy_fence();
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = *tmem_slot;
+  int min_lim = INT_MAX;
+#pragma unroll 1
+  for (int c = 0; c < N; ++c) min_lim = min(min_lim, lim[c]);
+  bool failed = false;                                     // this thread's wait gave up
+  const int tok0 = tile0 * T::TOK;                         // first token of the split
+
+  if (warp >= kSoftWarps && warp < kSoftWarps + kDeqWarps) {
+    // ---- dequantisation ----------------------------------------------------------
+    const int blk = warp & 3, half = (warp >> 2) & 1;
+    constexpr int W0 = (T::NW + 1) / 2;                    // index words of half 0 (half 1: the rest)
+    const int w_first = half ? W0 : 0, w_n = half ? T::NW - W0 : W0;
+    const int row = blk * 32 + lane;
+    const bool slot_ok = lane < T::LB;
+    // per position: byte 0 its entry's place in a table row, bytes 2-3 its place
+    // in a tile (below 32 KB)
+    uint32_t at[4 * W0];
+#pragma unroll
+    for (int w = 0; w < 4 * W0; ++w) {
+      const int j = (w_first * 4 + w + lane) % J;
+      at[w] = static_cast<uint32_t>(j * T::ENTRY) | (tile_off(row, j * T::ENTRY) << 16);
+    }
+    const uint8_t* pool_h = p.pool_lg + hkv * p.pool_stride_head;
+    const int32_t* bt = p.block_table + static_cast<int64_t>(lo) * p.max_pages_per_seq;
+    const int stage = blk >> 1;
+    // where this warp's block of tile i is: valid slots, and its address
+    auto entry_of = [&](int i) -> int {                    // page-table entry (warp-uniform), -1 past the end
+      const int b = (tile0 + i) * 4 + blk;
+      return (i < nt && b * T::LB < S) ? __ldg(bt + b / p.bpp) : -1;
+    };
+    auto load_rows = [&](int i, int entry, uint32_t (&kw)[W0], uint32_t (&vw)[W0]) -> int {
+      const int b = (tile0 + i) * 4 + blk;
+      int nv = i < nt ? max(0, min(T::LB, S - b * T::LB)) : 0;
+      if (nv > 0 && (entry < 0 || entry >= p.n_pages)) {
+        if (lane == 0 && p.status != nullptr) atomicOr(p.status, LOOPVQ_DECODE_STATUS_BAD_PAGE);
+        nv = 0;
+      }
+#pragma unroll
+      for (int w = 0; w < W0; ++w) kw[w] = vw[w] = 0u;
+      if (nv > 0 && slot_ok) {
+        const uint8_t* r = pool_h + static_cast<int64_t>(entry) * p.page_bytes + (b % p.bpp) * (T::LB * J) + lane * T::GR;
+        if constexpr (J == 32) {
+          const uint4 k4 = __ldcs(reinterpret_cast<const uint4*>(r + half * (T::LB * 16)));
+          const uint4 v4 = __ldcs(reinterpret_cast<const uint4*>(r + half * (T::LB * 16) + p.plane_bytes));
+          kw[0] = k4.x; kw[1] = k4.y; kw[2] = k4.z; kw[3] = k4.w;
+          vw[0] = v4.x; vw[1] = v4.y; vw[2] = v4.z; vw[3] = v4.w;
+        } else {
+#pragma unroll
+          for (int w = 0; w < W0; ++w) {
+            if (w < w_n) {
+              const int byte = (w_first + w) * 4;
+              const uint8_t* a = r + byte / T::GR * (T::LB * T::GR) + byte % T::GR;
+              kw[w] = __ldcs(reinterpret_cast<const uint32_t*>(a));
+              vw[w] = __ldcs(reinterpret_cast<const uint32_t*>(a + p.plane_bytes));
+            }
+          }
+        }
+      }
+      return nv;
+    };
+    uint32_t kw[W0], vw[W0];
+    int e_next = entry_of(0);
+    int nv = load_rows(0, e_next, kw, vw);
+    e_next = entry_of(1);
+#pragma unroll 1
+    for (int i = 0; i < nt && !failed; ++i) {
+      uint32_t kn[W0], vn[W0];
+      const int nv_next = load_rows(i + 1, e_next, kn, vn);   // lands while this tile is filled
+      e_next = entry_of(i + 2);
+      if (i > 0) failed = !mbar_wait(bar(kBarS0 + ((i - 1) & 1)), ((i - 1) >> 1) & 1, kShSpin);
+      if (__any_sync(0xffffffffu, failed)) { failed = true; break; }
+      fill_block<J, C, kKtabOff, kKtileOff, W0>(kw, at, w_n, nv, lane);
+      if (half == 0 && lane == 0) nvs[(i & 3) * 4 + blk] = nv;
+      proxy_fence();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarK));
+      if (i > 0) failed = !mbar_wait(bar(kBarVfree0 + stage), (i - 1) & 1, kShSpin);
+      if (__any_sync(0xffffffffu, failed)) { failed = true; break; }
+      fill_block<J, C, kVtabOff, kVtileOff, W0>(vw, at, w_n, nv, lane);
+      proxy_fence();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarV0 + stage));
+#pragma unroll
+      for (int w = 0; w < W0; ++w) {
+        kw[w] = kn[w];
+        vw[w] = vn[w];
+      }
+      nv = nv_next;
+    }
+  } else if (warp == kMmaWarp) {
+    // ---- the products --------------------------------------------------------------
+    if (lane == 0) {
+      const uint32_t kt = u32s(sm + kKtileOff), vt = u32s(sm + kVtileOff), qs = u32s(sm + kQOff), ps = u32s(sm + kPOff);
+      auto product_s = [&](int i) {                        // S^T of tile i
+        tc_after();
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s)
+          tc_mma_f16(tmem + kTmS + (i & 1) * 64, desc_sw128(kt + (s >> 2) * 1024 + (s & 3) * 32, 16, 2048),
+                     desc_sw128(qs + (s >> 2) * (N * 128) + (s & 3) * 32, 16, 1024), idesc_f16(N, 0, 0), s > 0 ? 1u : 0u);
+        tc_commit(bar(kBarS0 + (i & 1)));
+      };
+      failed = !mbar_wait(bar(kBarK), 0, kShSpin);
+      if (!failed) product_s(0);
+#pragma unroll 1
+      for (int i = 0; i < nt && !failed; ++i) {
+        if (i + 1 < nt) {
+          failed = !mbar_wait(bar(kBarK), (i + 1) & 1, kShSpin);
+          if (failed) break;
+          product_s(i + 1);
+        }
+        failed = !mbar_wait(bar(kBarP), i & 1, kShSpin);
+        if (failed) break;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {                      // O^T += V^T P over half the tile's rows
+          failed = failed || !mbar_wait(bar(kBarV0 + h), i & 1, kShSpin);
+          if (failed) break;
+          tc_after();
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+            tc_mma_f16(tmem + kTmO, desc_sw128(vt + (h * 4 + s) * 4096, 1024, 2048),
+                       desc_sw128(ps + (h * 4 + s) * 2048, 16, 1024), idesc_f16(N, 1, 1), (i > 0 || h > 0 || s > 0) ? 1u : 0u);
+          tc_commit(bar(kBarVfree0 + h));
+        }
+        if (failed) break;
+        tc_commit(bar(kBarO));
+      }
+      tc_commit(bar(kBarDrain));                           // everything issued so far
+    }
+    __syncwarp();
+  } else {
+    // ---- softmax -------------------------------------------------------------------
+    const int quad = warp & 3, half = warp >> 2, row = quad * 32 + lane, c0 = half * NC;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const int bar_id = 1 + half;                           // the four warps of a column half
+    float l[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) l[c] = 0.f;
+    int mb = 0;
+#pragma unroll 1
+    for (int i = 0; i < nt; ++i) {
+      failed = !mbar_wait(bar(kBarS0 + (i & 1)), (i >> 1) & 1, kShSpin);
+      __syncwarp();
+      tc_after();
+      uint32_t sv[NC];
+      tld<NC>(lanes + kTmS + (i & 1) * 64 + c0, sv);
+      tld_wait();
+      const int tok = tok0 + i * T::TOK + quad * T::LB + lane;
+      const bool valid = lane < nvs[(i & 3) * 4 + quad];
+      const bool masked = tok0 + (i + 1) * T::TOK > min_lim;   // some row ends inside this tile
+      const float* m = m_ref + mb * kMaxRows + c0;
+      float mx = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        if (!valid || (masked && tok >= lim[c0 + c])) sv[c] = 0xff800000u;   // -inf
+        mx = fmaxf(mx, fmaf(__uint_as_float(sv[c]), scale, -m[c]));
+      }
+      if (i > 0) failed = !mbar_wait(bar(kBarO), (i - 1) & 1, kShSpin) || failed;
+      tc_after();
+      if (named_or(bar_id, 128, mx > kRaise || failed)) {
+        if (named_or(bar_id, 128, failed)) {               // uniform over the four warps
+          failed = true;
+          break;
+        }
+        // raise the references that were passed; l and O^T shrink with them
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const float t = redux_fmax(__uint_as_float(sv[c]) * scale);
+          if (lane == 0) cm[quad * kMaxRows + c0 + c] = t;
+        }
+        named_sync(bar_id, 128);
+        float* mn = m_ref + (mb ^ 1) * kMaxRows + c0;
+        auto raised = [&](int c) {                         // the column's new reference
+          const float t = fmaxf(fmaxf(cm[c0 + c], cm[kMaxRows + c0 + c]),
+                                fmaxf(cm[2 * kMaxRows + c0 + c], cm[3 * kMaxRows + c0 + c]));
+          return t > m[c] + kRaise ? t - kTop : m[c];
+        };
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const float r = raised(c);
+          l[c] *= fast_exp2(m[c] - r);
+          if (quad == 0 && lane == 0) mn[c] = r;
+        }
+        if (i > 0) {
+#pragma unroll 1
+          for (int c = 0; c < NC; c += 8) {
+            uint32_t o[8];
+            tld<8>(lanes + kTmO + c0 + c, o);
+            tld_wait();
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              o[k] = __float_as_uint(__uint_as_float(o[k]) * fast_exp2(m[c + k] - raised(c + k)));
+            tst8(lanes + kTmO + c0 + c, o);
+          }
+          tst_wait();
+        }
+        mb ^= 1;
+        m = m_ref + mb * kMaxRows + c0;
+        named_sync(bar_id, 128);                           // the new references are written, cm is free
+      }
+#pragma unroll
+      for (int c = 0; c < NC; c += 8) {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float a = fast_exp2(fmaf(__uint_as_float(sv[c + 2 * k]), scale, -m[c + 2 * k]));
+          const float b = fast_exp2(fmaf(__uint_as_float(sv[c + 2 * k + 1]), scale, -m[c + 2 * k + 1]));
+          l[c + 2 * k] += a;
+          l[c + 2 * k + 1] += b;
+          w[k] = half2_bits(a, b);
+        }
+        *reinterpret_cast<uint4*>(sm + kPOff + row * 128 + ((((c0 + c) >> 3) ^ (row & 7)) << 4)) =
+            make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      proxy_fence();
+      tc_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarP));
+    }
+    if (!failed) failed = !mbar_wait(bar(kBarO), (nt - 1) & 1, kShSpin);
+    __syncwarp();
+    failed = named_or(bar_id, 128, failed);
+    if (!failed) {
+      // ---- the rows' records: o from TMEM (lane = channel), m and l ------------------
+      tc_after();
+      const float unscale = ldexpf(1.f, -kv);
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const float t = warp_sum(l[c]);
+        if (lane == 0) cm[quad * kMaxRows + c0 + c] = t;
+      }
+#pragma unroll 1
+      for (int c = 0; c < NC; c += 8) {
+        uint32_t o[8];
+        tld<8>(lanes + kTmO + c0 + c, o);
+        tld_wait();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (c0 + c + k < rows && row < D)
+            p.srec[(pair_of(c0 + c + k) * p.NS + split) * T::RS + 4 + row] = __uint_as_float(o[k]) * unscale;
+        }
+      }
+      named_sync(bar_id, 128);
+      if (quad == 0 && lane < NC && c0 + lane < rows) {
+        const int c = c0 + lane;
+        const float t = cm[c] + cm[kMaxRows + c] + cm[2 * kMaxRows + c] + cm[3 * kMaxRows + c];
+        float* rec = p.srec + (pair_of(c) * p.NS + split) * T::RS;
+        rec[0] = t == 0.f ? -INFINITY : m_ref[mb * kMaxRows + c];
+        rec[1] = t;
+      }
+    }
+  }
+  const bool any_failed = __syncthreads_or(failed);
+  if (any_failed) {
+    // a bounded wait gave up: wait for what was issued, flag, poison the records
+    if (tid == kMmaWarp * 32) {
+      const bool drained = mbar_wait(bar(kBarDrain), 0, kShDrainSpin);
+      if (p.status != nullptr)
+        atomicOr(p.status, drained ? LOOPVQ_DECODE_STATUS_TIMEOUT
+                                   : (LOOPVQ_DECODE_STATUS_TIMEOUT | LOOPVQ_DECODE_STATUS_UNDRAINED));
+    }
+    for (int c = tid; c < rows; c += kShThreads) {
+      float* rec = p.srec + (pair_of(c) * p.NS + split) * T::RS;
+      rec[0] = NAN;
+      rec[1] = 1.f;
+    }
+  }
+  tc_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmCols) : "memory");
+  }
+}
+
+// ---- own blocks ------------------------------------------------------------------
+
+// Per-warp scratch of an own block, in the tile area: value index rows (each
+// twice over, so that group j of slot k sits at byte J - k + j of its row), the
+// query twice over (so that lane i finds group (i + s) mod J at entry i + s), and
+// a block's softmax weights.
+constexpr int kOwnPitch = 80;                              // bytes of an index row (conflict-free 16-byte stores)
+constexpr int kOwnRows = 0;
+constexpr int kOwnQ = 32 * kOwnPitch;
+constexpr int kOwnP = kOwnQ + 1536;
+constexpr int kOwnBytes = kOwnP + 128;
+static_assert(kShWarps * kOwnBytes <= kMOff - kKtileOff, "own scratch fits the tile area");
+
+// Softmax state of one warp: m in log2 units; lane = (side, channel group j)
+// holds the o of group j over its side's tokens; l per lane (any share).
+template <int C>
+struct OwnState {
+  float m, l, o[C];
+};
+// Takes the warp's new maximum mx in.
+template <int C>
+__device__ __forceinline__ void own_raise(OwnState<C>& s, float mx) {
+  if (mx > s.m) {                                          // warp-uniform
+    const float f = s.m == -INFINITY ? 0.f : fast_exp2(s.m - mx);
+    s.l *= f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) s.o[c] *= f;
+    s.m = mx;
+  }
+}
+
+// The record of one task: sides joined, l summed over the warp.
+template <int J, int C>
+__device__ __forceinline__ void own_record(const OwnState<C>& s, float unscale, float* rec, int lane) {
+  constexpr int TPS = Shape<J, C>::TPS;
+  const float l = warp_sum(s.l);
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    float o = s.o[c];
+#pragma unroll
+    for (int k = 1; k < TPS; ++k) o += __shfl_sync(0xffffffffu, s.o[c], (lane + k * J) & 31);
+    if (lane < J) rec[4 + lane * C + c] = o * unscale;
+  }
+  if (lane == 0) {
+    rec[0] = l == l ? s.m : NAN;
+    rec[1] = l;
+  }
+}
+
+// bf16 window of (b, hkv): lane = C channels, 32/J tokens side by side, U steps
+// of loads ahead of the sums.
+template <int J, int C>
+__device__ void own_window(const SharedParams& p, int64_t head, int n_win, const float (&q)[C], float* rec, int lane) {
+  using T = Shape<J, C>;
+  constexpr int U = 8, D = T::D;
+  const int side = lane / J, j = lane % J;
+  const bool act = side < T::TPS;
+  OwnState<C> s;
+  s.m = -INFINITY;
+  s.l = 0.f;
+#pragma unroll
+  for (int c = 0; c < C; ++c) s.o[c] = 0.f;
+  const uint16_t* wk = p.win_k + head * p.W * D + j * C;
+  const uint16_t* wv = p.win_v + head * p.W * D + j * C;
+  uint32_t kr[U][C / 2], vr[U][C / 2];
+  auto request = [&](int n0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int n = n0 + u * T::TPS + side;
+      const bool ok = act && n < n_win;
+#pragma unroll
+      for (int c = 0; c < C / 2; ++c) {
+        kr[u][c] = ok ? __ldg(reinterpret_cast<const uint32_t*>(wk + static_cast<int64_t>(n) * D) + c) : 0u;
+        vr[u][c] = ok ? __ldg(reinterpret_cast<const uint32_t*>(wv + static_cast<int64_t>(n) * D) + c) : 0u;
+      }
+    }
+  };
+  request(0);
+#pragma unroll 1
+  for (int n0 = 0; n0 < n_win; n0 += U * T::TPS) {
+    float x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      x[u] = 0.f;
+#pragma unroll
+      for (int c = 0; c < C / 2; ++c) {
+        const float2 k = bf16x2_to_float2(kr[u][c]);
+        x[u] = fmaf(q[2 * c], k.x, fmaf(q[2 * c + 1], k.y, x[u]));
+      }
+    }
+    uint32_t v[U][C / 2];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int c = 0; c < C / 2; ++c) v[u][c] = vr[u][c];
+    if (n0 + U * T::TPS < n_win) request(n0 + U * T::TPS);
+    float mx = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {                          // sum over the side's J lanes
+      if constexpr ((J & (J - 1)) == 0) {
+#pragma unroll
+        for (int o = J / 2; o > 0; o >>= 1) x[u] += __shfl_xor_sync(0xffffffffu, x[u], o);
+      } else {
+        const int base = min(side, T::TPS - 1) * J;
+        float t = 0.f;
+#pragma unroll
+        for (int k = 0; k < J; ++k) t += __shfl_sync(0xffffffffu, x[u], base + k);
+        x[u] = t;
+      }
+      if (!act || n0 + u * T::TPS + side >= n_win) x[u] = -INFINITY;
+      mx = fmaxf(mx, x[u]);
+    }
+    own_raise<C>(s, redux_fmax(mx));
+    const float ref = s.m == -INFINITY ? 0.f : s.m;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float w = fast_exp2(x[u] - ref);
+      if (j == 0) s.l += w;                                // one lane of the side counts it
+#pragma unroll
+      for (int c = 0; c < C / 2; ++c) {
+        const float2 f = bf16x2_to_float2(v[u][c]);
+        s.o[2 * c] = fmaf(w, f.x, s.o[2 * c]);
+        s.o[2 * c + 1] = fmaf(w, f.y, s.o[2 * c + 1]);
+      }
+    }
+  }
+  own_record<J, C>(s, 1.f, rec, lane);
+}
+
+// Quantised tokens [t0, t1) of sequence b, a block of LB slots at a time.
+// Scores: lane = slot, byte s of its rotated key row is group (slot + s) mod J,
+// its codeword and the query's channels of that group come from shared memory
+// without bank conflicts. Values: lane = (side, group j), token by token.
+template <int J, int C>
+__device__ void own_chunk(const SharedParams& p, const uint8_t* pool_h, int b, int t0, int t1, float unscale,
+                          unsigned char* scratch, float* rec, int lane) {
+  using T = Shape<J, C>;
+  constexpr int LB = T::LB, NW = T::NW;
+  const int side = lane / J, j = lane % J;
+  const bool act = side < T::TPS;
+  const uint32_t sa = u32s(scratch);
+  float* pw = reinterpret_cast<float*>(scratch + kOwnP);
+  OwnState<C> s;
+  s.m = -INFINITY;
+  s.l = 0.f;
+#pragma unroll
+  for (int c = 0; c < C; ++c) s.o[c] = 0.f;
+  const int32_t* bt = p.block_table + static_cast<int64_t>(b) * p.max_pages_per_seq;
+  const int b0 = t0 / LB, b1 = (t1 + LB - 1) / LB;
+  uint32_t kw[NW], vw[NW];
+  auto entry_of = [&](int blk) { return blk < b1 ? __ldg(bt + blk / p.bpp) : -1; };
+  bool ok = false;
+  auto request = [&](int blk, int entry) {                 // index rows of a block; false: nothing to read
+    ok = blk < b1 && entry >= 0 && entry < p.n_pages;
+    if (blk < b1 && !ok && lane == 0 && p.status != nullptr) atomicOr(p.status, LOOPVQ_DECODE_STATUS_BAD_PAGE);
+#pragma unroll
+    for (int w = 0; w < NW; ++w) kw[w] = vw[w] = 0u;
+    if (!ok || lane >= LB) return;
+    const uint8_t* r = pool_h + static_cast<int64_t>(entry) * p.page_bytes + (blk % p.bpp) * (LB * J) + lane * T::GR;
+#pragma unroll
+    for (int w = 0; w < NW; w += T::GR / 4) {
+      const uint8_t* a = r + w * 4 / T::GR * (LB * T::GR);
+      if constexpr (T::GR == 16) {
+        const uint4 k4 = __ldcs(reinterpret_cast<const uint4*>(a));
+        const uint4 v4 = __ldcs(reinterpret_cast<const uint4*>(a + p.plane_bytes));
+        kw[w] = k4.x; kw[w + 1] = k4.y; kw[w + 2] = k4.z; kw[w + 3] = k4.w;
+        vw[w] = v4.x; vw[w + 1] = v4.y; vw[w + 2] = v4.z; vw[w + 3] = v4.w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < T::GR / 4; ++i) {
+          kw[w + i] = __ldcs(reinterpret_cast<const uint32_t*>(a) + i);
+          vw[w + i] = __ldcs(reinterpret_cast<const uint32_t*>(a + p.plane_bytes) + i);
+        }
+      }
+    }
+  };
+  uint32_t at[NW];                                         // entry bytes of this slot's groups, packed
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    at[w] = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) at[w] |= static_cast<uint32_t>((4 * w + i + lane) % J * T::ENTRY) << (8 * i);
+  }
+  int e_next = entry_of(b0);
+  request(b0, e_next);
+  e_next = entry_of(b0 + 1);
+#pragma unroll 1
+  for (int blk = b0; blk < b1; ++blk) {
+    // the value rows of this block, each twice
+    __syncwarp();
+    {
+      const uint32_t row = sa + kOwnRows + lane * kOwnPitch;
+      if constexpr (J == 32 || J == 16) {
+#pragma unroll
+        for (int rep = 0; rep < 2; ++rep)
+#pragma unroll
+          for (int w = 0; w < NW; w += 4) {
+            Word<16> t;
+            t.w[0] = vw[w]; t.w[1] = vw[w + 1]; t.w[2] = vw[w + 2]; t.w[3] = vw[w + 3];
+            sts<16, 0>(row + rep * J + w * 4, t);
+          }
+      } else {
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(row + w * 4), "r"(vw[w]) : "memory");
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(row + J + w * 4), "r"(vw[w]) : "memory");
+        }
+      }
+    }
+    const int tok = blk * LB + lane;
+    const bool valid = ok && lane < LB && tok >= t0 && tok < t1;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      Word<T::ENTRY> e[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)                          // (entry byte, codeword row)
+        e[i] = lds<T::ENTRY, kShBase + kKtabOff>(__byte_perm(kw[w], at[w], (4u + i) | (static_cast<uint32_t>(i) << 4)) & 0xffffu);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t qa = sa + kOwnQ + (lane + 4 * w + i) * (C * 4);
+#pragma unroll
+        for (int c = 0; c < C; c += 4) {
+          const Word<16> qv = lds<16, 0>(qa + c * 4);
+          const float2 k0 = half2_floats(e[i].w[c / 2]), k1 = half2_floats(e[i].w[c / 2 + 1]);
+          acc[i] = fmaf(__uint_as_float(qv.w[0]), k0.x, fmaf(__uint_as_float(qv.w[1]), k0.y, acc[i]));
+          acc[i] = fmaf(__uint_as_float(qv.w[2]), k1.x, fmaf(__uint_as_float(qv.w[3]), k1.y, acc[i]));
+        }
+      }
+    }
+    request(blk + 1, e_next);                              // lands under this block's values
+    e_next = entry_of(blk + 2);
+    const float x = valid ? (acc[0] + acc[1]) + (acc[2] + acc[3]) : -INFINITY;
+    own_raise<C>(s, redux_fmax(x));
+    const float w0 = fast_exp2(x - (s.m == -INFINITY ? 0.f : s.m));
+    s.l += w0;
+    pw[lane] = w0;
+    __syncwarp();
+    if (act) {
+      const uint32_t row = sa + kOwnRows + side * J * kOwnPitch + j;
+      const uint32_t wa = sa + kOwnP + side * J * 4;
+#pragma unroll
+      for (int k = 0; k < J; k += 4) {
+        const Word<16> w4 = lds<16, 0>(wa + k * 4);
+        uint32_t iv[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          asm volatile("ld.shared.u8 %0, [%1];" : "=r"(iv[i]) : "r"(row + (k + i) * kOwnPitch + J - (k + i)));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const Word<T::ENTRY> e = lds<T::ENTRY, kShBase + kVtabOff>(iv[i] * 256u + j * T::ENTRY);
+          const float w = __uint_as_float(w4.w[i]);
+#pragma unroll
+          for (int c = 0; c < C; c += 2) {
+            const float2 f = half2_floats(e.w[c / 2]);
+            s.o[c] = fmaf(w, f.x, s.o[c]);
+            s.o[c + 1] = fmaf(w, f.y, s.o[c + 1]);
+          }
+        }
+      }
+    }
+  }
+  own_record<J, C>(s, unscale, rec, lane);
+}
+
+template <int J, int C>
+__device__ void own_block(const SharedParams& p, unsigned char* sm, int unit) {
+  using T = Shape<J, C>;
+  constexpr int D = T::D;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  float* red = reinterpret_cast<float*>(sm + kRedOff);
+  const int hkv = unit % p.Hkv, part = unit / p.Hkv;
+  const int kk = load_table<J, C, kKtabOff>(p.cb_k + hkv * p.cb_stride_head, red, tid);
+  const int kv = load_table<J, C, kVtabOff>(p.cb_v + hkv * p.cb_stride_head, red, tid);
+  __syncthreads();
+  const float unk = ldexpf(1.f, -kk), unv = ldexpf(1.f, -kv);
+  unsigned char* scratch = sm + kKtileOff + warp * kOwnBytes;
+  float* qs = reinterpret_cast<float*>(scratch + kOwnQ);
+  const uint8_t* pool_h = p.pool_lg + hkv * p.pool_stride_head;
+  const int64_t tasks = static_cast<int64_t>(p.B) * p.ratio * p.NC;
+  for (int64_t t = static_cast<int64_t>(part) * kShWarps + warp; t < tasks;
+       t += static_cast<int64_t>(p.own_parts) * kShWarps) {
+    const int ck = static_cast<int>(t % p.NC) - 1;         // -1: the window
+    const int64_t y = t / p.NC;
+    const int r = static_cast<int>(y % p.ratio), b = static_cast<int>(y / p.ratio);
+    const int64_t pair = static_cast<int64_t>(b) * p.Hq + hkv * p.ratio + r;
+    const int n_vq = seq_vq(p, b);
+    const int g = group_of(p, b, lane);
+    const int s0 = g < 0 ? 0 : min(group_shared(p, g), n_vq);
+    const int n_own = min(n_vq - s0, p.max_own);
+    float* rec = p.orec + (pair * p.NC + ck + 1) * T::RS;
+    if (ck < 0) {
+      if (hkv == 0 && r == 0 && lane == 0 && n_own < n_vq - s0 && p.status != nullptr)
+        atomicOr(p.status, LOOPVQ_DECODE_STATUS_BAD_GROUP);
+      float q[C];
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        q[c] = lane / J < T::TPS ? bf16_bits_to_float(p.q[pair * D + lane % J * C + c]) * p.scale_log2 : 0.f;
+      own_window<J, C>(p, static_cast<int64_t>(b) * p.Hkv + hkv, max(0, min(__ldg(p.seq_lens + b), p.W)), q, rec, lane);
+      continue;
+    }
+    const int t0 = s0 + ck * p.CH, t1 = min(s0 + n_own, t0 + p.CH);
+    if (t0 >= t1) continue;                                // the merge does not read it
+    __syncwarp();
+    static_assert((31 + J) * C * 4 <= kOwnP - kOwnQ, "query entries 0 .. 30 + J fit");
+    for (int i = lane; i < (31 + J) * C; i += 32) qs[i] = bf16_bits_to_float(p.q[pair * D + i % D]) * p.scale_log2 * unk;
+    __syncwarp();
+    own_chunk<J, C>(p, pool_h, b, t0, t1, unv, scratch, rec, lane);
+  }
+}
+
+template <int J, int C, int N>
+__global__ void __launch_bounds__(kShThreads, 1) shared_attn_kernel(const SharedParams p) {
+  extern __shared__ __align__(1024) unsigned char sm[];
+  if (u32s(sm) != kShBase) {                          // the host checks this before launching
+    if (threadIdx.x == 0 && p.status != nullptr) atomicOr(p.status, LOOPVQ_DECODE_STATUS_SHARED_BASE);
+    return;
+  }
+  const int unit = blockIdx.x;
+  if (unit < p.shared_blocks)
+    shared_block<J, C, N>(p, sm, unit);
+  else
+    own_block<J, C>(p, sm, unit - p.shared_blocks);
+}
+
+// One warp per (sequence, query head): joins the records that its blocks wrote.
+template <int D>
+__global__ void __launch_bounds__(128) shared_merge_kernel(const SharedParams p) {
+  constexpr int RS = 4 + D, NCH = (D + 31) / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t pair = static_cast<int64_t>(blockIdx.x) * 4 + warp;
+  if (pair >= static_cast<int64_t>(p.B) * p.Hq) return;
+  const int b = static_cast<int>(pair / p.Hq);
+  const int n_vq = seq_vq(p, b);
+  const int g = group_of(p, b, lane);
+  const int s0 = g < 0 ? 0 : min(group_shared(p, g), n_vq);
+  const int n_own = min(n_vq - s0, p.max_own);
+  const int ns = g < 0 ? 0 : p.NS, nc = 1 + (n_own + p.CH - 1) / p.CH;   // the window's record first
+  float m = -INFINITY, l = 0.f, o[NCH];
+#pragma unroll
+  for (int c = 0; c < NCH; ++c) o[c] = 0.f;
+  for (int r0 = 0; r0 < ns + nc; r0 += 4) {
+    float mr[4], lr[4], v[4][NCH];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = r0 + k;
+      mr[k] = -INFINITY;
+      lr[k] = 0.f;
+      const float* rec = r < ns ? p.srec + (pair * p.NS + r) * RS : p.orec + (pair * p.NC + r - ns) * RS;
+      const bool ok = r < ns + nc;
+      if (ok) {
+        mr[k] = __ldcg(rec);
+        lr[k] = __ldcg(rec + 1);
+      }
+#pragma unroll
+      for (int c = 0; c < NCH; ++c) {
+        const int ch = c * 32 + lane;
+        v[k][c] = ok && ch < D ? __ldcg(rec + 4 + ch) : 0.f;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (mr[k] == -INFINITY) continue;                    // an empty record
+      const float mn = fmaxf(m, mr[k]);
+      const float f0 = m == -INFINITY ? 0.f : fast_exp2(m - mn), f1 = fast_exp2(mr[k] - mn);
+      l = fmaf(l, f0, lr[k] * f1);
+#pragma unroll
+      for (int c = 0; c < NCH; ++c) o[c] = fmaf(o[c], f0, v[k][c] * f1);
+      m = mn;
+    }
+  }
+  const float inv = (l > 0.f) ? 1.f / l : (l == 0.f ? 0.f : l);   // NaN stays NaN
+#pragma unroll
+  for (int c = 0; c < NCH; ++c) {
+    const int ch = c * 32 + lane;
+    if (ch < D) static_cast<__nv_bfloat16*>(p.out)[pair * D + ch] = __float2bfloat16_rn(o[c] * inv);
+  }
+  if (lane == 0 && p.lse != nullptr) p.lse[pair] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// How a call is cut up; a function of the sizes alone, so that the workspace
+// can be sized without a device.
+struct SharedPlan {
+  int N, RT, NS, NC, CH, own_parts;
+  int64_t shared_blocks;
+};
+constexpr int kPlanSms = 148;             // blocks that run at once (one per SM of a B200)
+
+SharedPlan make_plan(const Geometry& g, int batch, int n_groups, int max_group, int max_shared, int max_own) {
+  SharedPlan q{};
+  const int ratio = g.Hq / g.Hkv;
+  const int64_t rows = static_cast<int64_t>(max_group) * ratio;
+  q.N = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  q.RT = static_cast<int>((rows + q.N - 1) / q.N);
+  q.CH = 128;
+  while ((max_own + q.CH - 1) / q.CH > 64) q.CH *= 2;
+  q.NC = 1 + (max_own + q.CH - 1) / q.CH;                  // the window, and the chunks
+  const int tiles = (max_shared + 4 * g.LB - 1) / (4 * g.LB);
+  const int64_t units = max_shared > 0 ? static_cast<int64_t>(n_groups) * q.RT * g.Hkv : 0;
+  const int64_t tasks = static_cast<int64_t>(batch) * ratio * q.NC;      // warps' tasks of one head
+  // rough block times (cycles): setup, a tile, a task of a whole chunk
+  const double setup = 6000, t_tile = 1800, t_task = 6000;
+  const double work_a = units * (tiles * t_tile), work_b = g.Hkv * (tasks * t_task / kShWarps);
+  int parts = static_cast<int>(kPlanSms / g.Hkv * work_b / (work_a + work_b + 1) + 0.5);
+  if (parts < 1) parts = 1;
+  const int64_t most = (tasks + kShWarps - 1) / kShWarps;
+  int64_t room = kPlanSms - static_cast<int64_t>(parts) * g.Hkv;
+  q.NS = 1;
+  if (units > 0) {
+    if (room >= units) {
+      q.NS = static_cast<int>(room / units);
+    } else {                                               // several waves: the split with the least idle tail
+      double best = 0;
+      for (int ns = 1; ns <= 8; ++ns) {
+        const double waves = static_cast<double>((units * ns + kPlanSms - 1) / kPlanSms);
+        const double t = waves * (setup + (tiles + ns - 1) / ns * t_tile);
+        if (ns == 1 || t < best) {
+          best = t;
+          q.NS = ns;
+        }
+      }
+      parts = static_cast<int>(work_b / g.Hkv / (setup + (tiles + q.NS - 1) / q.NS * t_tile) + 1);
+    }
+    if (q.NS > tiles) q.NS = tiles;
+    if (q.NS > 64) q.NS = 64;
+  }
+  q.own_parts = static_cast<int>(parts < most ? parts : most);
+  q.shared_blocks = units * q.NS;
+  return q;
+}
+
+template <int J, int C, int N>
+loopvq_status launch_shared_n(const SharedParams& p, cudaStream_t st) {
+  static std::atomic<uint64_t> configured{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return LOOPVQ_ERR_CUDA;
+  const uint64_t bit = (dev >= 0 && dev < 64) ? (1ull << dev) : 0ull;
+  auto kernel = shared_attn_kernel<J, C, N>;
+  if (bit == 0 || !(configured.load(std::memory_order_relaxed) & bit)) {
+    int reserved = -1;
+    if (cudaDeviceGetAttribute(&reserved, cudaDevAttrReservedSharedMemoryPerBlock, dev) != cudaSuccess)
+      return LOOPVQ_ERR_CUDA;
+    cudaFuncAttributes fa{};
+    if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess) return LOOPVQ_ERR_CUDA;
+    if (reserved != static_cast<int>(kShBase) || fa.sharedSizeBytes != 0) return LOOPVQ_ERR_UNSUPPORTED;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kShSmem) != cudaSuccess)
+      return LOOPVQ_ERR_CUDA;
+    configured.fetch_or(bit, std::memory_order_relaxed);
+  }
+  const int64_t blocks = static_cast<int64_t>(p.shared_blocks) + static_cast<int64_t>(p.Hkv) * p.own_parts;
+  kernel<<<static_cast<unsigned>(blocks), kShThreads, kShSmem, st>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return LOOPVQ_ERR_CUDA;
+  const int64_t pairs = static_cast<int64_t>(p.B) * p.Hq;
+  shared_merge_kernel<J * C><<<static_cast<unsigned>((pairs + 3) / 4), 128, 0, st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? LOOPVQ_OK : LOOPVQ_ERR_CUDA;
+}
+
+template <int J, int C>
+loopvq_status launch_shared_jc(const SharedParams& p, int N, cudaStream_t st) {
+  switch (N) {
+    case 16: return launch_shared_n<J, C, 16>(p, st);
+    case 32: return launch_shared_n<J, C, 32>(p, st);
+    default: return launch_shared_n<J, C, 64>(p, st);
+  }
+}
+
+size_t record_bytes(const Geometry& g, int batch, int slots) {
+  return static_cast<size_t>(batch) * g.Hq * slots * (4 + g.d) * sizeof(float);
+}
+
+}  // namespace
+
+bool shared_attn_supported(const Geometry& g, int n_groups, int out_dtype) {
+  if (out_dtype != LOOPVQ_DTYPE_BF16 || n_groups == 0) return false;
+  switch (g.J * 100 + g.c) {
+    case 3204: case 1604: case 1208: case 1608: case 2404: return true;
+    default: return false;
+  }
+}
+
+size_t shared_attn_workspace_bytes(const Geometry& g, int batch, int n_groups, int max_group, int max_shared,
+                                   int max_own) {
+  const SharedPlan q = make_plan(g, batch, n_groups, max_group, max_shared, max_own);
+  return kStatusBytes + record_bytes(g, batch, q.NS) + record_bytes(g, batch, q.NC);
+}
+
+loopvq_status launch_shared_attn(const SharedArgs& a) {
+  const Geometry& g = *a.geo;
+  const SharedPlan q = make_plan(g, a.batch, a.n_groups, a.max_group, a.max_shared, a.max_own);
+  if (q.shared_blocks + static_cast<int64_t>(g.Hkv) * q.own_parts > INT_MAX / 2) return LOOPVQ_ERR_UNSUPPORTED;
+  const int gamma = a.loop_step / g.g, tau = a.loop_step % g.g;
+  SharedParams p{};
+  p.q = static_cast<const uint16_t*>(a.q);
+  p.pool_lg = a.pool + a.layer * g.pool_stride_layer + gamma * g.pool_stride_group;
+  p.pool_stride_head = g.pool_stride_head;
+  p.page_bytes = g.page_bytes;
+  p.plane_bytes = g.plane_bytes;
+  p.cb_k = a.codebooks + a.layer * g.cb_stride_layer + gamma * g.cb_stride_group + tau * g.cb_stride_loop;
+  p.cb_v = p.cb_k + g.cb_stride_kv;
+  p.cb_stride_head = g.cb_stride_head;
+  p.block_table = a.block_table;
+  p.seq_lens = a.seq_lens;
+  p.group_starts = a.group_starts;
+  p.shared_lens = a.shared_lens;
+  p.win_k = static_cast<const uint16_t*>(a.win_k);
+  p.win_v = static_cast<const uint16_t*>(a.win_v);
+  char* ws = static_cast<char*>(a.workspace);
+  p.status = reinterpret_cast<int*>(ws);
+  p.srec = reinterpret_cast<float*>(ws + kStatusBytes);
+  p.orec = reinterpret_cast<float*>(ws + kStatusBytes + record_bytes(g, a.batch, q.NS));
+  p.out = a.out;
+  p.lse = a.lse;
+  p.B = a.batch;
+  p.n_groups = a.n_groups;
+  p.Hq = g.Hq;
+  p.Hkv = g.Hkv;
+  p.ratio = g.Hq / g.Hkv;
+  p.W = g.W;
+  p.Pg = g.Pg;
+  p.n_pages = g.n_pages;
+  p.max_pages_per_seq = g.max_pages_per_seq;
+  p.max_group = a.max_group;
+  p.max_shared = a.max_shared;
+  p.max_own = a.max_own;
+  p.NS = q.NS;
+  p.RT = q.RT;
+  p.NC = q.NC;
+  p.CH = q.CH;
+  p.shared_blocks = static_cast<int>(q.shared_blocks);
+  p.own_parts = q.own_parts;
+  p.bpp = g.Pg / g.LB;
+  p.scale_log2 = a.sm_scale * kLog2e;
+  cudaStream_t st = static_cast<cudaStream_t>(a.stream);
+  switch (g.J * 100 + g.c) {
+    case 3204: return launch_shared_jc<32, 4>(p, q.N, st);
+    case 1604: return launch_shared_jc<16, 4>(p, q.N, st);
+    case 1208: return launch_shared_jc<12, 8>(p, q.N, st);
+    case 1608: return launch_shared_jc<16, 8>(p, q.N, st);
+    case 2404: return launch_shared_jc<24, 4>(p, q.N, st);
+    default: return LOOPVQ_ERR_UNSUPPORTED;
+  }
+}
+
+}  // namespace loopvq

@@ -172,13 +172,16 @@ def test_a_sequence_without_any_valid_page_uses_its_window():
 
 def test_other_stream_replay_and_repeat():
     c = SharedCase(MHA, [(5, 700)], [40, 0, 77, 3, 150], seed=21)
-    out, lse = c.run_gpu()
+    out, lse = c.run_gpu(bounds=(c.max_group, c.max_shared, c.max_own + 100))
     d = c.device()
     cfg = c.config()
     o = torch.empty(c.B, 2, 128, dtype=torch.bfloat16, device="cuda")
-    ws = torch.zeros(c.workspace_bytes(), dtype=torch.uint8, device="cuda")
+    # (bounds that hold for the lengths of the first and of the last call)
+    most = c.max_own + 100
+    ws = torch.zeros(L.loopvq_decode_shared_workspace_bytes(cfg, c.B, 1, c.max_group, c.max_shared, most),
+                     dtype=torch.uint8, device="cuda")
     call = lambda **kw: L.loopvq_decode_attn_shared(cfg, 0, c.t, **d, out=o, workspace=ws, max_group=c.max_group,
-                                                    max_shared_len=c.max_shared, max_own_len=c.max_own,
+                                                    max_shared_len=c.max_shared, max_own_len=most,
                                                     sm_scale=c.sm_scale, **kw)
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
@@ -205,4 +208,27 @@ def test_other_stream_replay_and_repeat():
     c2.groups, c2.S = [(5, 600)], [600] * 5
     lse2 = np.array([[c2.oracle(b, h)[1] for h in range(2)] for b in range(5)])
     check_shared(c2, o.float().cpu().numpy(), lse2)
-    assert int(ws[:4].view(torch.int32)) in (0, B.LOOPVQ_DECODE_STATUS_BAD_GROUP)
+    assert int(ws[:4].view(torch.int32)) == 0
+
+
+def test_values_past_the_bounds_are_clipped_and_flagged():
+    c = SharedCase(MHA, [(3, 500)], [130, 4, 60], seed=22)
+    flag = B.LOOPVQ_DECODE_STATUS_BAD_GROUP
+    # own tokens past max_own_len are left out: the oracle without them
+    out, lse = c.run_gpu(status=flag, bounds=(3, 500, 60))
+    c.n_vq = [560, 504, 560]
+    check_shared(c, out, lse)
+    # a sequence past max_group shares nothing, and its own tokens are clipped too
+    c = SharedCase(MHA, [(3, 500)], [60, 4, 60], seed=22)
+    out, lse = c.run_gpu(status=flag, bounds=(2, 500, 60))
+    c.n_vq[2] = 60
+    check_shared(c, out, lse)
+    # starts outside the batch: its sequences share nothing
+    d = c.device()
+    d["group_starts"].copy_(torch.tensor([-1, 9], dtype=torch.int32))
+    out, _ = c.run_gpu(status=flag, dev_inputs=d)
+    assert np.all(np.isfinite(out))
+    d["group_starts"].copy_(torch.tensor([5, 2], dtype=torch.int32))
+    out, lse = c.run_gpu(status=flag, dev_inputs=d)
+    c.n_vq = [60, 60, 60]
+    check_shared(c, out, lse)
