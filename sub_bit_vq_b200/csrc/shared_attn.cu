@@ -83,7 +83,7 @@ constexpr int kVtabOff = kTabBytes;
 constexpr int kKtileOff = 2 * kTabBytes;                   // [16 row groups][2 channel blocks][8][128 B]
 constexpr int kTileBytes = kTileRows * 256;
 constexpr int kVtileOff = kKtileOff + kTileBytes;
-constexpr int kPOff = kVtileOff + kTileBytes;              // [128 tokens][128 B], up to 64 rows of fp16
+constexpr int kPOff = kVtileOff + kTileBytes;              // [128 tokens] rows of 128 B, or twice of 64 B
 constexpr int kQOff = kPOff + kTileRows * 128;             // [2 channel blocks][N][128 B]
 constexpr int kQBytes = kMaxRows * 256;
 constexpr int kMOff = kQOff + kQBytes;                     // float [2][64]: references
@@ -92,11 +92,11 @@ constexpr int kLimOff = kCmOff + 4 * kMaxRows * 4;         // int [64]: a row's 
 constexpr int kNvOff = kLimOff + kMaxRows * 4;             // int [4 tiles][4 blocks]: valid slots
 constexpr int kRedOff = kNvOff + 64;                       // float [17]: block reduction
 constexpr int kBarOff = kRedOff + 96;                      // mbarriers
-constexpr int kTmemSlotOff = kBarOff + 96;
+constexpr int kTmemSlotOff = kBarOff + 112;
 constexpr int kShSmem = kTmemSlotOff + 16;
 static_assert(kShSmem <= 227 * 1024, "shared memory above 227 KB");
 
-enum { kBarK = 0, kBarS0, kBarS1, kBarP, kBarV0, kBarV1, kBarVfree0, kBarVfree1, kBarO, kBarDrain, kBars };
+enum { kBarK = 0, kBarS0, kBarS1, kBarP0, kBarP1, kBarV0, kBarV1, kBarVfree0, kBarVfree1, kBarO0, kBarO1, kBarTab, kBarDrain, kBars };
 
 constexpr uint32_t kTmCols = 256, kTmS = 0, kTmO = 128;    // TMEM columns: S^T twice 64, O^T 64
 
@@ -113,6 +113,8 @@ struct SharedParams {
   const int32_t* shared_lens;
   const uint16_t* win_k;
   const uint16_t* win_v;
+  const unsigned char* tables;    // [Hkv][K, V] fp16 tables of kTabBytes
+  const int* exps;                // [Hkv][K, V][32]: a group's table entries are scaled by 2^exps
   float* srec;                    // [pairs][NS][4 + d] records of the shared blocks
   float* orec;                    // [pairs][NC][4 + d] records of the own chunks
   int* status;
@@ -122,7 +124,7 @@ struct SharedParams {
   int max_group, max_shared, max_own;
   int NS, RT, NC, CH;             // splits, row tiles, own records (window, chunks), tokens of a chunk
   int shared_blocks, own_parts;   // grid: shared blocks, then Hkv * own_parts own blocks
-  int bpp;                        // index blocks of a page
+  int lbpp;                       // log2 of the index blocks of a page
   float scale_log2;
 };
 
@@ -138,10 +140,29 @@ struct Shape {
   static constexpr int TPS = 32 / J;                   // tokens a warp takes side by side (own tokens)
 };
 
-// K-major or M-major operand in the 128-byte swizzle.
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  return static_cast<uint64_t>((saddr >> 4) & 0x3fffu) | (static_cast<uint64_t>(lbo >> 4) << 16) |
-         (static_cast<uint64_t>(sbo >> 4) << 32) | (1ull << 46) | (2ull << 61);
+// Shared-memory operand descriptors, low and high word: address and leading
+// offset; stride offset, version and swizzle.
+constexpr uint32_t kSw128 = 2u, kSw64 = 4u;
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
+  return ((saddr >> 4) & 0x3fffu) | ((lbo >> 4) << 16);
+}
+__device__ __forceinline__ constexpr uint32_t desc_hi(uint32_t sbo, uint32_t swizzle) {
+  return (sbo >> 4) | (1u << 14) | (swizzle << 29);
+}
+__device__ __forceinline__ void tc_mma_f16_words(uint32_t tmem_d, uint32_t alo, uint32_t ahi, uint32_t blo, uint32_t bhi,
+                                                 uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %6, 0;\n mov.b64 a, {%1, %2};\n mov.b64 b, {%3, %4};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n}\n" ::"r"(tmem_d), "r"(alo), "r"(ahi), "r"(blo),
+      "r"(bhi), "r"(idesc), "r"(accumulate) : "memory");
+}
+// Whether the barrier's phase of the given parity has completed (no wait).
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred P;\n mbarrier.test_wait.parity.shared::cta.b64 P, [%1], %2;\n selp.u32 %0, 1, 0, P;\n}\n"
+      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0u;
 }
 // f16 x f16 -> f32, M = 128; ta, tb: operand is M-major (N-major).
 __device__ __forceinline__ uint32_t idesc_f16(int n, uint32_t ta, uint32_t tb) {
@@ -257,55 +278,61 @@ __device__ __forceinline__ float finite_abs(float v) {
   return a < INFINITY ? a : 0.f;
 }
 
-// One codebook slice [J][E][C] (float32) into an fp16 table, entries scaled by
-// 2^k (returned). Every thread calls it; the caller synchronises.
-template <int J, int C, int TAB>
-__device__ int load_table(const float* cb, float* red, int tid) {
-  constexpr int N = kE * J;                                // entries
-  constexpr int PER = (N + kShThreads - 1) / kShThreads;
-  constexpr int F4 = C / 4;
-  float4 v[PER][F4];
-  auto entry = [&](int k, int& e, int& j) {                // thread's k-th entry: 16 groups x 2 codewords a warp
-    const int f = tid + k * kShThreads;
-    if constexpr (J % 16 == 0) {
-      const int w = f >> 5, l = f & 31;
-      j = (w % (J / 16)) * 16 + (l & 15);
-      e = (w / (J / 16)) * 2 + (l >> 4);
-    } else {
-      e = f / J;
-      j = f - e * J;
-    }
-    return f < N;
-  };
-  float top = 0.f;
+// The codebook slices of one call as fp16 tables: block (4 channel groups, K or
+// V, head), thread = codeword. Each group is scaled by a power of two of its
+// own. Blocks of the attention grid start meanwhile and wait for this grid.
+template <int J, int C>
+__global__ void __launch_bounds__(kE) shared_table_kernel(const float* cb_k, const float* cb_v, int64_t cb_stride_head,
+                                                          unsigned char* tables, int* exps) {
+  __shared__ float red[4][kE / 32];
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int j0 = blockIdx.x * 4, kv = blockIdx.y, h = blockIdx.z, e = threadIdx.x;
+  const float* cb = (kv ? cb_v : cb_k) + h * cb_stride_head;
+  float4 v[4][C / 4];
 #pragma unroll
-  for (int k = 0; k < PER; ++k) {
-    int e, j;
-    if (entry(k, e, j)) {
+  for (int k = 0; k < 4; ++k)
 #pragma unroll
-      for (int i = 0; i < F4; ++i) {
-        v[k][i] = __ldg(reinterpret_cast<const float4*>(cb + (static_cast<size_t>(j) * kE + e) * C) + i);
-        top = fmaxf(fmaxf(top, fmaxf(finite_abs(v[k][i].x), finite_abs(v[k][i].y))),
-                    fmaxf(finite_abs(v[k][i].z), finite_abs(v[k][i].w)));
-      }
+    for (int i = 0; i < C / 4; ++i)
+      v[k][i] = __ldg(reinterpret_cast<const float4*>(cb + (static_cast<size_t>(j0 + k) * kE + e) * C) + i);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < C / 4; ++i)
+      top = fmaxf(fmaxf(top, fmaxf(finite_abs(v[k][i].x), finite_abs(v[k][i].y))),
+                  fmaxf(finite_abs(v[k][i].z), finite_abs(v[k][i].w)));
+    top = redux_fmax(top);
+    if ((e & 31) == 0) red[k][e >> 5] = top;
+  }
+  __syncthreads();
+  uint32_t w[2 * C];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < kE / 32; ++i) top = fmaxf(top, red[k][i]);
+    const int ex = scale_exp(top);
+    const float f = ldexpf(1.f, ex);
+    if (e == 0) exps[(h * 2 + kv) * 32 + j0 + k] = ex;
+#pragma unroll
+    for (int i = 0; i < C / 4; ++i) {
+      w[k * (C / 2) + 2 * i] = half2_bits(v[k][i].x * f, v[k][i].y * f);
+      w[k * (C / 2) + 2 * i + 1] = half2_bits(v[k][i].z * f, v[k][i].w * f);
     }
   }
-  const int ex = scale_exp(block_max(top, red, tid));
-  const float f = ldexpf(1.f, ex);
+  uint4* dst = reinterpret_cast<uint4*>(tables + (static_cast<size_t>(h) * 2 + kv) * kTabBytes + e * 256 + j0 * 2 * C);
 #pragma unroll
-  for (int k = 0; k < PER; ++k) {
-    int e, j;
-    if (entry(k, e, j)) {
-      Word<2 * C> w;
-#pragma unroll
-      for (int i = 0; i < F4; ++i) {
-        w.w[2 * i] = half2_bits(v[k][i].x * f, v[k][i].y * f);
-        w.w[2 * i + 1] = half2_bits(v[k][i].z * f, v[k][i].w * f);
-      }
-      sts<2 * C, kShBase + TAB>(e * 256 + j * 2 * C, w);
-    }
-  }
-  return ex;
+  for (int i = 0; i < C / 2; ++i) dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+}
+
+// Requests both tables of a head into shared memory (one thread).
+__device__ __forceinline__ void request_tables(const SharedParams& p, unsigned char* sm, int hkv, uint32_t bar) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(2 * kTabBytes) : "memory");
+  const unsigned char* src = p.tables + static_cast<size_t>(hkv) * 2 * kTabBytes;
+  for (int part = 0; part < 4; ++part)
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     u32s(sm + kKtabOff + part * (kTabBytes / 2))),
+                 "l"(src + part * (kTabBytes / 2)), "r"(kTabBytes / 2), "r"(bar) : "memory");
 }
 
 // Quantised tokens of sequence b.
@@ -364,6 +391,8 @@ template <int J, int C, int N>
 __device__ void shared_block(const SharedParams& p, unsigned char* sm, int unit) {
   using T = Shape<J, C>;
   constexpr int D = T::D, NC = N / 2;
+  // P: rows of 64 query rows and one buffer, or of 32 and two (the same bytes)
+  constexpr int PP = N > 32 ? 128 : 64, PB = N > 32 ? 1 : 2;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   float* m_ref = reinterpret_cast<float*>(sm + kMOff);
   float* cm = reinterpret_cast<float*>(sm + kCmOff);
@@ -406,7 +435,9 @@ __device__ void shared_block(const SharedParams& p, unsigned char* sm, int unit)
   // ---- setup: barriers, TMEM, tables, queries -----------------------------------
   if (tid == 0) {
     for (int i = 0; i < kBars; ++i) {
-      const uint32_t n = i == kBarK ? kDeqWarps : i == kBarP ? kSoftWarps : (i == kBarV0 || i == kBarV1) ? kDeqWarps / 2 : 1;
+      const uint32_t n = i == kBarK ? kDeqWarps
+                         : (i == kBarP0 || i == kBarP1) ? kSoftWarps
+                         : (i == kBarV0 || i == kBarV1) ? kDeqWarps / 2 : 1;
       asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar(i)), "r"(n) : "memory");
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -416,24 +447,29 @@ __device__ void shared_block(const SharedParams& p, unsigned char* sm, int unit)
                  "r"(kTmCols) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  const int kk = load_table<J, C, kKtabOff>(p.cb_k + hkv * p.cb_stride_head, red, tid);
-  const int kv = load_table<J, C, kVtabOff>(p.cb_v + hkv * p.cb_stride_head, red, tid);
-  // the queries, scaled into fp16: piece = 8 channels of a row
+  asm volatile("griddepcontrol.wait;" ::: "memory");       // the tables are written
+  if (tid == 0) request_tables(p, sm, hkv, bar(kBarTab));
+  const int* exk = p.exps + hkv * 64;
+  // the queries, scaled into fp16 (against the scales of the key groups): piece =
+  // 8 channels of a row
   int kq;
   {
     constexpr int PIECES = N * D / 8, PER = (PIECES + kShThreads - 1) / kShThreads;
-    uint4 v[PER];
+    float v[PER][8];
     float top = 0.f;
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
       const int f = tid + k * kShThreads, c = f / (D / 8), part = f % (D / 8);
-      v[k] = make_uint4(0u, 0u, 0u, 0u);
-      if (f < PIECES && c < rows) v[k] = *(reinterpret_cast<const uint4*>(p.q + pair_of(c) * D) + part);
-      const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+      uint4 t = make_uint4(0u, 0u, 0u, 0u);
+      if (f < PIECES && c < rows) t = *(reinterpret_cast<const uint4*>(p.q + pair_of(c) * D) + part);
+      const uint32_t w[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
+        const float f2 = ldexpf(1.f, f < PIECES ? -__ldg(exk + (part * 8 + 2 * i) / C) : 0);
         const float2 a = bf16x2_to_float2(w[i]);
-        top = fmaxf(top, fmaxf(finite_abs(a.x), finite_abs(a.y)));
+        v[k][2 * i] = a.x * f2;
+        v[k][2 * i + 1] = a.y * f2;
+        top = fmaxf(top, fmaxf(finite_abs(v[k][2 * i]), finite_abs(v[k][2 * i + 1])));
       }
     }
     kq = scale_exp(block_max(top, red, tid));
@@ -442,18 +478,12 @@ __device__ void shared_block(const SharedParams& p, unsigned char* sm, int unit)
     for (int k = 0; k < PER; ++k) {
       const int f = tid + k * kShThreads, c = f / (D / 8), byte = (f % (D / 8)) * 16;
       if (f >= PIECES) continue;
-      const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-      uint32_t h[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 a = bf16x2_to_float2(w[i]);
-        h[i] = half2_bits(a.x * f2, a.y * f2);
-      }
       *reinterpret_cast<uint4*>(sm + kQOff + (byte >> 7) * (N * 128) + c * 128 + ((byte & 127) ^ ((c & 7) << 4))) =
-          make_uint4(h[0], h[1], h[2], h[3]);
+          make_uint4(half2_bits(v[k][0] * f2, v[k][1] * f2), half2_bits(v[k][2] * f2, v[k][3] * f2),
+                     half2_bits(v[k][4] * f2, v[k][5] * f2), half2_bits(v[k][6] * f2, v[k][7] * f2));
     }
   }
-  const float scale = ldexpf(p.scale_log2, -kk - kq);
+  const float scale = ldexpf(p.scale_log2, -kq);
   // a row's shared tokens, its unset reference, zero value rows past a block's slots
   for (int c = tid; c < N; c += kShThreads) {
     lim[c] = c < rows ? min(S, seq_vq(p, static_cast<int>(pair_of(c) / p.Hq))) : INT_MAX;
@@ -495,7 +525,7 @@ __device__ void shared_block(const SharedParams& p, unsigned char* sm, int unit)
     // where this warp's block of tile i is: valid slots, and its address
     auto entry_of = [&](int i) -> int {                    // page-table entry (warp-uniform), -1 past the end
       const int b = (tile0 + i) * 4 + blk;
-      return (i < nt && b * T::LB < S) ? __ldg(bt + b / p.bpp) : -1;
+      return (i < nt && b * T::LB < S) ? __ldg(bt + (b >> p.lbpp)) : -1;
     };
     auto load_rows = [&](int i, int entry, uint32_t (&kw)[W0], uint32_t (&vw)[W0]) -> int {
       const int b = (tile0 + i) * 4 + blk;
@@ -507,7 +537,7 @@ __device__ void shared_block(const SharedParams& p, unsigned char* sm, int unit)
 #pragma unroll
       for (int w = 0; w < W0; ++w) kw[w] = vw[w] = 0u;
       if (nv > 0 && slot_ok) {
-        const uint8_t* r = pool_h + static_cast<int64_t>(entry) * p.page_bytes + (b % p.bpp) * (T::LB * J) + lane * T::GR;
+        const uint8_t* r = pool_h + static_cast<int64_t>(entry) * p.page_bytes + (b & ((1 << p.lbpp) - 1)) * (T::LB * J) + lane * T::GR;
         if constexpr (J == 32) {
           const uint4 k4 = __ldcs(reinterpret_cast<const uint4*>(r + half * (T::LB * 16)));
           const uint4 v4 = __ldcs(reinterpret_cast<const uint4*>(r + half * (T::LB * 16) + p.plane_bytes));
@@ -527,71 +557,94 @@ __device__ void shared_block(const SharedParams& p, unsigned char* sm, int unit)
       }
       return nv;
     };
-    uint32_t kw[W0], vw[W0];
-    int e_next = entry_of(0);
-    int nv = load_rows(0, e_next, kw, vw);
-    e_next = entry_of(1);
-#pragma unroll 1
-    for (int i = 0; i < nt && !failed; ++i) {
-      uint32_t kn[W0], vn[W0];
-      const int nv_next = load_rows(i + 1, e_next, kn, vn);   // lands while this tile is filled
-      e_next = entry_of(i + 2);
-      if (i > 0) failed = !mbar_wait(bar(kBarS0 + ((i - 1) & 1)), ((i - 1) >> 1) & 1, kShSpin);
-      if (__any_sync(0xffffffffu, failed)) { failed = true; break; }
+    // K runs one tile ahead of V: while the softmax of tile i is under way its
+    // scores' successor is already on the tensor cores
+    uint32_t kw[W0], vw[W0], vn[W0];                       // K rows of tile i + 1, V rows of tiles i and i + 1
+    auto fill_k = [&](int i, int nv) {
       fill_block<J, C, kKtabOff, kKtileOff, W0>(kw, at, w_n, nv, lane);
       if (half == 0 && lane == 0) nvs[(i & 3) * 4 + blk] = nv;
       proxy_fence();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarK));
-      if (i > 0) failed = !mbar_wait(bar(kBarVfree0 + stage), (i - 1) & 1, kShSpin);
-      if (__any_sync(0xffffffffu, failed)) { failed = true; break; }
-      fill_block<J, C, kVtabOff, kVtileOff, W0>(vw, at, w_n, nv, lane);
-      proxy_fence();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarV0 + stage));
+    };
+    int e_next = entry_of(0);
+    int nv = load_rows(0, e_next, kw, vw);
+    e_next = entry_of(1);
+    failed = !mbar_wait(bar(kBarTab), 0, kShSpin);
+    if (!__any_sync(0xffffffffu, failed)) {
+      fill_k(0, nv);
+      int nv_next = load_rows(1, e_next, kw, vn);
+      e_next = entry_of(2);
+#pragma unroll 1
+      for (int i = 0; i < nt; ++i) {
+        uint32_t kl[W0], vl[W0];
+        const int nv_last = load_rows(i + 2, e_next, kl, vl);   // lands while this tile is filled
+        e_next = entry_of(i + 3);
+        if (i + 1 < nt) {
+          failed = !mbar_wait(bar(kBarS0 + (i & 1)), (i >> 1) & 1, kShSpin);
+          if (__any_sync(0xffffffffu, failed)) break;
+          fill_k(i + 1, nv_next);
+        }
+        if (i > 0) failed = !mbar_wait(bar(kBarVfree0 + stage), (i - 1) & 1, kShSpin);
+        if (__any_sync(0xffffffffu, failed)) break;
+        fill_block<J, C, kVtabOff, kVtileOff, W0>(vw, at, w_n, nv, lane);
+        proxy_fence();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarV0 + stage));
 #pragma unroll
-      for (int w = 0; w < W0; ++w) {
-        kw[w] = kn[w];
-        vw[w] = vn[w];
+        for (int w = 0; w < W0; ++w) {
+          kw[w] = kl[w];
+          vw[w] = vn[w];
+          vn[w] = vl[w];
+        }
+        nv = nv_next;
+        nv_next = nv_last;
       }
-      nv = nv_next;
     }
+    failed = __any_sync(0xffffffffu, failed);
   } else if (warp == kMmaWarp) {
     // ---- the products --------------------------------------------------------------
     if (lane == 0) {
-      const uint32_t kt = u32s(sm + kKtileOff), vt = u32s(sm + kVtileOff), qs = u32s(sm + kQOff), ps = u32s(sm + kPOff);
-      auto product_s = [&](int i) {                        // S^T of tile i
-        tc_after();
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s)
-          tc_mma_f16(tmem + kTmS + (i & 1) * 64, desc_sw128(kt + (s >> 2) * 1024 + (s & 3) * 32, 16, 2048),
-                     desc_sw128(qs + (s >> 2) * (N * 128) + (s & 3) * 32, 16, 1024), idesc_f16(N, 0, 0), s > 0 ? 1u : 0u);
-        tc_commit(bar(kBarS0 + (i & 1)));
-      };
-      failed = !mbar_wait(bar(kBarK), 0, kShSpin);
-      if (!failed) product_s(0);
+      // descriptors: the high words are constant, the low words the address plus
+      // an immediate
+      const uint32_t k_hi = desc_hi(2048, kSw128), q_hi = desc_hi(1024, kSw128), v_hi = desc_hi(2048, kSw128);
+      const uint32_t p_hi = desc_hi(PP * 8, PP == 128 ? kSw128 : kSw64);
+      const uint32_t k_lo = desc_lo(u32s(sm + kKtileOff), 16), q_lo = desc_lo(u32s(sm + kQOff), 16);
+      const uint32_t v_lo = desc_lo(u32s(sm + kVtileOff), 1024), p_lo = desc_lo(u32s(sm + kPOff), 16);
+      int ns = 0, no = 0, spin = 0;                        // next scores, next output
 #pragma unroll 1
-      for (int i = 0; i < nt && !failed; ++i) {
-        if (i + 1 < nt) {
-          failed = !mbar_wait(bar(kBarK), (i + 1) & 1, kShSpin);
-          if (failed) break;
-          product_s(i + 1);
-        }
-        failed = !mbar_wait(bar(kBarP), i & 1, kShSpin);
-        if (failed) break;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {                      // O^T += V^T P over half the tile's rows
-          failed = failed || !mbar_wait(bar(kBarV0 + h), i & 1, kShSpin);
-          if (failed) break;
+      while (no < nt && !failed) {
+        bool idle = true;
+        // S^T of tile ns: its buffer is free once P of tile ns - 2 is written
+        if (ns < nt && ns <= no + 1 && mbar_test(bar(kBarK), ns & 1)) {
           tc_after();
+          const uint32_t d = tmem + kTmS + (ns & 1) * 64;
 #pragma unroll
-          for (int s = 0; s < 4; ++s)
-            tc_mma_f16(tmem + kTmO, desc_sw128(vt + (h * 4 + s) * 4096, 1024, 2048),
-                       desc_sw128(ps + (h * 4 + s) * 2048, 16, 1024), idesc_f16(N, 1, 1), (i > 0 || h > 0 || s > 0) ? 1u : 0u);
-          tc_commit(bar(kBarVfree0 + h));
+          for (int s = 0; s < D / 16; ++s)
+            tc_mma_f16_words(d, k_lo + ((s >> 2) * 1024 + (s & 3) * 32) / 16, k_hi,
+                             q_lo + ((s >> 2) * (N * 128) + (s & 3) * 32) / 16, q_hi, idesc_f16(N, 0, 0), s > 0 ? 1u : 0u);
+          tc_commit(bar(kBarS0 + (ns & 1)));
+          ++ns;
+          idle = false;
         }
-        if (failed) break;
-        tc_commit(bar(kBarO));
+        // O^T += V^T P of tile no
+        if (no < ns && mbar_test(bar(kBarP0 + no % PB), (no / PB) & 1) && mbar_test(bar(kBarV0), no & 1) &&
+            mbar_test(bar(kBarV1), no & 1)) {
+          tc_after();
+          const uint32_t pb = p_lo + (no % PB) * (kTileRows * PP) / 16;
+#pragma unroll
+          for (int s = 0; s < 8; ++s) {
+            tc_mma_f16_words(tmem + kTmO, v_lo + s * 4096 / 16, v_hi, pb + s * (16 * PP) / 16, p_hi, idesc_f16(N, 1, 1),
+                             (no > 0 || s > 0) ? 1u : 0u);
+            if (s == 3) tc_commit(bar(kBarVfree0));
+          }
+          tc_commit(bar(kBarVfree1));
+          tc_commit(bar(kBarO0 + (no & 1)));
+          ++no;
+          idle = false;
+        }
+        spin = idle ? spin + 1 : 0;
+        failed = spin >= kShSpin;
       }
       tc_commit(bar(kBarDrain));                           // everything issued so far
     }
@@ -612,24 +665,39 @@ __device__ void shared_block(const SharedParams& p, unsigned char* sm, int unit)
       tc_after();
       uint32_t sv[NC];
       tld<NC>(lanes + kTmS + (i & 1) * 64 + c0, sv);
-      tld_wait();
-      const int tok = tok0 + i * T::TOK + quad * T::LB + lane;
-      const bool valid = lane < nvs[(i & 3) * 4 + quad];
-      const bool masked = tok0 + (i + 1) * T::TOK > min_lim;   // some row ends inside this tile
+      const int nv = nvs[(i & 3) * 4 + quad];
       const float* m = m_ref + mb * kMaxRows + c0;
+      float4 m4[NC / 4];
+#pragma unroll
+      for (int c = 0; c < NC / 4; ++c) m4[c] = *reinterpret_cast<const float4*>(m + 4 * c);
+      tld_wait();
+      if (nv < 32 && lane >= nv) {                         // no token in this slot
+#pragma unroll
+        for (int c = 0; c < NC; ++c) sv[c] = 0xff800000u;  // -inf
+      }
+      if (tok0 + (i + 1) * T::TOK > min_lim) {             // some row ends inside this tile
+        const int tok = tok0 + i * T::TOK + quad * T::LB + lane;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+          if (tok >= lim[c0 + c]) sv[c] = 0xff800000u;
+      }
       float mx = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        if (!valid || (masked && tok >= lim[c0 + c])) sv[c] = 0xff800000u;   // -inf
-        mx = fmaxf(mx, fmaf(__uint_as_float(sv[c]), scale, -m[c]));
+      for (int c = 0; c < NC; c += 4) {
+        mx = fmaxf(mx, fmaxf(fmaf(__uint_as_float(sv[c]), scale, -m4[c / 4].x),
+                             fmaf(__uint_as_float(sv[c + 1]), scale, -m4[c / 4].y)));
+        mx = fmaxf(mx, fmaxf(fmaf(__uint_as_float(sv[c + 2]), scale, -m4[c / 4].z),
+                             fmaf(__uint_as_float(sv[c + 3]), scale, -m4[c / 4].w)));
       }
-      if (i > 0) failed = !mbar_wait(bar(kBarO), (i - 1) & 1, kShSpin) || failed;
-      tc_after();
+      if (i >= PB) failed = !mbar_wait(bar(kBarO0 + ((i - PB) & 1)), ((i - PB) >> 1) & 1, kShSpin) || failed;
       if (named_or(bar_id, 128, mx > kRaise || failed)) {
+        if (PB == 2 && i > 0) failed = !mbar_wait(bar(kBarO0 + ((i - 1) & 1)), ((i - 1) >> 1) & 1, kShSpin) || failed;
         if (named_or(bar_id, 128, failed)) {               // uniform over the four warps
           failed = true;
           break;
         }
+        __syncwarp();
+        tc_after();
         // raise the references that were passed; l and O^T shrink with them
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
@@ -663,35 +731,38 @@ __device__ void shared_block(const SharedParams& p, unsigned char* sm, int unit)
           tst_wait();
         }
         mb ^= 1;
-        m = m_ref + mb * kMaxRows + c0;
         named_sync(bar_id, 128);                           // the new references are written, cm is free
+#pragma unroll
+        for (int c = 0; c < NC / 4; ++c) m4[c] = *reinterpret_cast<const float4*>(m_ref + mb * kMaxRows + c0 + 4 * c);
       }
+      unsigned char* prow = sm + kPOff + (i % PB) * (kTileRows * PP) + row * PP;
+      const int swz = PP == 128 ? row & 7 : (row >> 1) & 3;
 #pragma unroll
       for (int c = 0; c < NC; c += 8) {
         uint32_t w[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float a = fast_exp2(fmaf(__uint_as_float(sv[c + 2 * k]), scale, -m[c + 2 * k]));
-          const float b = fast_exp2(fmaf(__uint_as_float(sv[c + 2 * k + 1]), scale, -m[c + 2 * k + 1]));
+          const float4 mm = m4[(c + 2 * k) / 4];
+          const float a = fast_exp2(fmaf(__uint_as_float(sv[c + 2 * k]), scale, -((k & 1) ? mm.z : mm.x)));
+          const float b = fast_exp2(fmaf(__uint_as_float(sv[c + 2 * k + 1]), scale, -((k & 1) ? mm.w : mm.y)));
           l[c + 2 * k] += a;
           l[c + 2 * k + 1] += b;
           w[k] = half2_bits(a, b);
         }
-        *reinterpret_cast<uint4*>(sm + kPOff + row * 128 + ((((c0 + c) >> 3) ^ (row & 7)) << 4)) =
-            make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(prow + ((((c0 + c) >> 3) ^ swz) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
       }
       proxy_fence();
       tc_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarP));
+      if (lane == 0) mbar_arrive(bar(kBarP0 + i % PB));
     }
-    if (!failed) failed = !mbar_wait(bar(kBarO), (nt - 1) & 1, kShSpin);
+    if (!failed) failed = !mbar_wait(bar(kBarO0 + ((nt - 1) & 1)), ((nt - 1) >> 1) & 1, kShSpin);
     __syncwarp();
     failed = named_or(bar_id, 128, failed);
     if (!failed) {
       // ---- the rows' records: o from TMEM (lane = channel), m and l ------------------
       tc_after();
-      const float unscale = ldexpf(1.f, -kv);
+      const float unscale = row < D ? ldexpf(1.f, -__ldg(exk + 32 + row / C)) : 0.f;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         const float t = warp_sum(l[c]);
@@ -722,7 +793,7 @@ __device__ void shared_block(const SharedParams& p, unsigned char* sm, int unit)
   if (any_failed) {
     // a bounded wait gave up: wait for what was issued, flag, poison the records
     if (tid == kMmaWarp * 32) {
-      const bool drained = mbar_wait(bar(kBarDrain), 0, kShDrainSpin);
+      const bool drained = mbar_wait(bar(kBarDrain), 0, kShDrainSpin) && mbar_wait(bar(kBarTab), 0, kShDrainSpin);
       if (p.status != nullptr)
         atomicOr(p.status, drained ? LOOPVQ_DECODE_STATUS_TIMEOUT
                                    : (LOOPVQ_DECODE_STATUS_TIMEOUT | LOOPVQ_DECODE_STATUS_UNDRAINED));
@@ -891,7 +962,7 @@ __device__ void own_chunk(const SharedParams& p, const uint8_t* pool_h, int b, i
   const int32_t* bt = p.block_table + static_cast<int64_t>(b) * p.max_pages_per_seq;
   const int b0 = t0 / LB, b1 = (t1 + LB - 1) / LB;
   uint32_t kw[NW], vw[NW];
-  auto entry_of = [&](int blk) { return blk < b1 ? __ldg(bt + blk / p.bpp) : -1; };
+  auto entry_of = [&](int blk) { return blk < b1 ? __ldg(bt + (blk >> p.lbpp)) : -1; };
   bool ok = false;
   auto request = [&](int blk, int entry) {                 // index rows of a block; false: nothing to read
     ok = blk < b1 && entry >= 0 && entry < p.n_pages;
@@ -899,7 +970,7 @@ __device__ void own_chunk(const SharedParams& p, const uint8_t* pool_h, int b, i
 #pragma unroll
     for (int w = 0; w < NW; ++w) kw[w] = vw[w] = 0u;
     if (!ok || lane >= LB) return;
-    const uint8_t* r = pool_h + static_cast<int64_t>(entry) * p.page_bytes + (blk % p.bpp) * (LB * J) + lane * T::GR;
+    const uint8_t* r = pool_h + static_cast<int64_t>(entry) * p.page_bytes + (blk & ((1 << p.lbpp) - 1)) * (LB * J) + lane * T::GR;
 #pragma unroll
     for (int w = 0; w < NW; w += T::GR / 4) {
       const uint8_t* a = r + w * 4 / T::GR * (LB * T::GR);
@@ -1011,12 +1082,24 @@ __device__ void own_block(const SharedParams& p, unsigned char* sm, int unit) {
   using T = Shape<J, C>;
   constexpr int D = T::D;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  float* red = reinterpret_cast<float*>(sm + kRedOff);
   const int hkv = unit % p.Hkv, part = unit / p.Hkv;
-  const int kk = load_table<J, C, kKtabOff>(p.cb_k + hkv * p.cb_stride_head, red, tid);
-  const int kv = load_table<J, C, kVtabOff>(p.cb_v + hkv * p.cb_stride_head, red, tid);
+  const uint32_t bar = u32s(sm + kBarOff);
+  if (tid == 0) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(1u) : "memory");
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
   __syncthreads();
-  const float unk = ldexpf(1.f, -kk), unv = ldexpf(1.f, -kv);
+  asm volatile("griddepcontrol.wait;" ::: "memory");       // the tables are written
+  if (tid == 0) request_tables(p, sm, hkv, bar);
+  const bool failed = __syncthreads_or(!mbar_wait(bar, 0, kShSpin));
+  if (failed && tid == 0) {                                // no copy may outlive the block
+    const bool drained = mbar_wait(bar, 0, kShDrainSpin);
+    if (p.status != nullptr)
+      atomicOr(p.status, drained ? LOOPVQ_DECODE_STATUS_TIMEOUT
+                                 : (LOOPVQ_DECODE_STATUS_TIMEOUT | LOOPVQ_DECODE_STATUS_UNDRAINED));
+  }
+  const int* exk = p.exps + hkv * 64;
+  const float unv = lane < J ? ldexpf(1.f, -__ldg(exk + 32 + lane)) : 0.f;   // of this lane's record channels
   unsigned char* scratch = sm + kKtileOff + warp * kOwnBytes;
   float* qs = reinterpret_cast<float*>(scratch + kOwnQ);
   const uint8_t* pool_h = p.pool_lg + hkv * p.pool_stride_head;
@@ -1032,6 +1115,13 @@ __device__ void own_block(const SharedParams& p, unsigned char* sm, int unit) {
     const int s0 = g < 0 ? 0 : min(group_shared(p, g), n_vq);
     const int n_own = min(n_vq - s0, p.max_own);
     float* rec = p.orec + (pair * p.NC + ck + 1) * T::RS;
+    if (failed) {
+      if (lane == 0) {
+        rec[0] = NAN;
+        rec[1] = 1.f;
+      }
+      continue;
+    }
     if (ck < 0) {
       if (hkv == 0 && r == 0 && lane == 0 && n_own < n_vq - s0 && p.status != nullptr)
         atomicOr(p.status, LOOPVQ_DECODE_STATUS_BAD_GROUP);
@@ -1046,7 +1136,8 @@ __device__ void own_block(const SharedParams& p, unsigned char* sm, int unit) {
     if (t0 >= t1) continue;                                // the merge does not read it
     __syncwarp();
     static_assert((31 + J) * C * 4 <= kOwnP - kOwnQ, "query entries 0 .. 30 + J fit");
-    for (int i = lane; i < (31 + J) * C; i += 32) qs[i] = bf16_bits_to_float(p.q[pair * D + i % D]) * p.scale_log2 * unk;
+    for (int i = lane; i < (31 + J) * C; i += 32) 
+      qs[i] = ldexpf(bf16_bits_to_float(p.q[pair * D + i % D]) * p.scale_log2, -__ldg(exk + i % D / C));
     __syncwarp();
     own_chunk<J, C>(p, pool_h, b, t0, t1, unv, scratch, rec, lane);
   }
@@ -1191,7 +1282,21 @@ loopvq_status launch_shared_n(const SharedParams& p, cudaStream_t st) {
     configured.fetch_or(bit, std::memory_order_relaxed);
   }
   const int64_t blocks = static_cast<int64_t>(p.shared_blocks) + static_cast<int64_t>(p.Hkv) * p.own_parts;
-  kernel<<<static_cast<unsigned>(blocks), kShThreads, kShSmem, st>>>(p);
+  shared_table_kernel<J, C><<<dim3(J / 4, 2, p.Hkv), kE, 0, st>>>(p.cb_k, p.cb_v, p.cb_stride_head,
+                                                                  const_cast<unsigned char*>(p.tables),
+                                                                  const_cast<int*>(p.exps));
+  if (cudaGetLastError() != cudaSuccess) return LOOPVQ_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(kShThreads);
+  cfg.dynamicSmemBytes = kShSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) return LOOPVQ_ERR_CUDA;
   if (cudaGetLastError() != cudaSuccess) return LOOPVQ_ERR_CUDA;
   const int64_t pairs = static_cast<int64_t>(p.B) * p.Hq;
   shared_merge_kernel<J * C><<<static_cast<unsigned>((pairs + 3) / 4), 128, 0, st>>>(p);
@@ -1224,7 +1329,8 @@ bool shared_attn_supported(const Geometry& g, int n_groups, int out_dtype) {
 size_t shared_attn_workspace_bytes(const Geometry& g, int batch, int n_groups, int max_group, int max_shared,
                                    int max_own) {
   const SharedPlan q = make_plan(g, batch, n_groups, max_group, max_shared, max_own);
-  return kStatusBytes + record_bytes(g, batch, q.NS) + record_bytes(g, batch, q.NC);
+  return kStatusBytes + record_bytes(g, batch, q.NS) + record_bytes(g, batch, q.NC) +
+         static_cast<size_t>(g.Hkv) * (2 * kTabBytes + 64 * sizeof(int));
 }
 
 loopvq_status launch_shared_attn(const SharedArgs& a) {
@@ -1251,6 +1357,9 @@ loopvq_status launch_shared_attn(const SharedArgs& a) {
   p.status = reinterpret_cast<int*>(ws);
   p.srec = reinterpret_cast<float*>(ws + kStatusBytes);
   p.orec = reinterpret_cast<float*>(ws + kStatusBytes + record_bytes(g, a.batch, q.NS));
+  char* tables = reinterpret_cast<char*>(p.orec) + record_bytes(g, a.batch, q.NC);
+  p.tables = reinterpret_cast<unsigned char*>(tables);
+  p.exps = reinterpret_cast<int*>(tables + static_cast<size_t>(g.Hkv) * 2 * kTabBytes);
   p.out = a.out;
   p.lse = a.lse;
   p.B = a.batch;
@@ -1271,7 +1380,7 @@ loopvq_status launch_shared_attn(const SharedArgs& a) {
   p.CH = q.CH;
   p.shared_blocks = static_cast<int>(q.shared_blocks);
   p.own_parts = q.own_parts;
-  p.bpp = g.Pg / g.LB;
+  while ((1 << p.lbpp) < g.Pg / g.LB) ++p.lbpp;
   p.scale_log2 = a.sm_scale * kLog2e;
   cudaStream_t st = static_cast<cudaStream_t>(a.stream);
   switch (g.J * 100 + g.c) {
