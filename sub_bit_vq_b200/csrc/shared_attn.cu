@@ -57,11 +57,14 @@
 namespace loopvq {
 namespace {
 
-constexpr int kShWarps = 17;
+constexpr int kSoftWarps = 8;             // warps 0-7
+constexpr int kDeqWarps = 8;              // warps 8-15 fill the K tile, 16-23 the V tile
+constexpr int kKWarp = kSoftWarps, kVWarp = kKWarp + kDeqWarps, kMmaWarp = kVWarp + kDeqWarps;
+constexpr int kShWarps = kMmaWarp + 1;
 constexpr int kShThreads = kShWarps * 32;
-constexpr int kSoftWarps = 8;
-constexpr int kDeqWarps = 8;
-constexpr int kMmaWarp = 16;
+// Registers of a thread: 72 at launch. With 64 query rows the softmax warps need
+// more and take what the filling warps give (8 x 104 + 16 x 56 = 24 x 72).
+constexpr int kSoftRegs = 104, kDeqRegs = 56;
 constexpr int kTileRows = 128;            // token rows of a tile (4 index blocks of up to 32 slots)
 constexpr int kMaxRows = 64;              // query rows of a block
 constexpr float kRaise = 14.f;            // log2: a weight reaches 2^14 at most
@@ -90,13 +93,16 @@ constexpr int kMOff = kQOff + kQBytes;                     // float [2][64]: ref
 constexpr int kCmOff = kMOff + 2 * kMaxRows * 4;           // float [4][64]: column maxima, then sums
 constexpr int kLimOff = kCmOff + 4 * kMaxRows * 4;         // int [64]: a row's shared tokens
 constexpr int kNvOff = kLimOff + kMaxRows * 4;             // int [4 tiles][4 blocks]: valid slots
-constexpr int kRedOff = kNvOff + 64;                       // float [17]: block reduction
-constexpr int kBarOff = kRedOff + 96;                      // mbarriers
-constexpr int kTmemSlotOff = kBarOff + 112;
+constexpr int kRedOff = kNvOff + 64;                       // float [25]: block reduction
+constexpr int kBarOff = kRedOff + 112;                     // mbarriers
+constexpr int kTmemSlotOff = kBarOff + 96;
 constexpr int kShSmem = kTmemSlotOff + 16;
 static_assert(kShSmem <= 227 * 1024, "shared memory above 227 KB");
 
-enum { kBarK = 0, kBarS0, kBarS1, kBarP0, kBarP1, kBarV0, kBarV1, kBarVfree0, kBarVfree1, kBarO0, kBarO1, kBarTab, kBarDrain, kBars };
+// K and V tile filled, S^T done (per buffer; its K tile is free), P written (per
+// buffer), O^T += done (by tile parity; its V tile and P are free).
+enum { kBarK = 0, kBarV, kBarS0, kBarS1, kBarP0, kBarP1, kBarO0, kBarO1, kBarTab, kBarDrain, kBars };
+static_assert(kBars * 8 <= kTmemSlotOff - kBarOff, "barriers fit");
 
 constexpr uint32_t kTmCols = 256, kTmS = 0, kTmO = 128;    // TMEM columns: S^T twice 64, O^T 64
 
@@ -123,7 +129,7 @@ struct SharedParams {
   int B, n_groups, Hq, Hkv, ratio, W, Pg, n_pages, max_pages_per_seq;
   int max_group, max_shared, max_own;
   int NS, RT, NC, CH;             // splits, row tiles, own records (window, chunks), tokens of a chunk
-  int shared_blocks, own_parts;   // grid: shared blocks, then Hkv * own_parts own blocks
+  int shared_blocks, own_parts;   // grids: shared blocks; Hkv * own_parts own blocks
   int lbpp;                       // log2 of the index blocks of a page
   float scale_log2;
 };
@@ -155,14 +161,6 @@ __device__ __forceinline__ void tc_mma_f16_words(uint32_t tmem_d, uint32_t alo, 
       "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %6, 0;\n mov.b64 a, {%1, %2};\n mov.b64 b, {%3, %4};\n"
       " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n}\n" ::"r"(tmem_d), "r"(alo), "r"(ahi), "r"(blo),
       "r"(bhi), "r"(idesc), "r"(accumulate) : "memory");
-}
-// Whether the barrier's phase of the given parity has completed (no wait).
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred P;\n mbarrier.test_wait.parity.shared::cta.b64 P, [%1], %2;\n selp.u32 %0, 1, 0, P;\n}\n"
-      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-  return ok != 0u;
 }
 // f16 x f16 -> f32, M = 128; ta, tb: operand is M-major (N-major).
 __device__ __forceinline__ uint32_t idesc_f16(int n, uint32_t ta, uint32_t tb) {
@@ -239,6 +237,10 @@ __device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+template <int R>
+__device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R>
+__device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("barrier.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
@@ -422,7 +424,10 @@ __device__ void shared_block(const SharedParams& p, unsigned char* sm, int unit)
     const int r = rt * N + c;
     return static_cast<int64_t>(lo + r / p.ratio) * p.Hq + hkv * p.ratio + r % p.ratio;
   };
-  if (rows <= 0) return;                                   // block-uniform
+  if (rows <= 0 || nt <= 0) {                              // block-uniform
+    asm volatile("griddepcontrol.wait;" ::: "memory");     // (the own grid relies on it)
+  }
+  if (rows <= 0) return;
   if (nt <= 0) {
     for (int c = tid; c < rows; c += kShThreads) {
       float* rec = p.srec + (pair_of(c) * p.NS + split) * T::RS;
@@ -435,9 +440,9 @@ __device__ void shared_block(const SharedParams& p, unsigned char* sm, int unit)
   // ---- setup: barriers, TMEM, tables, queries -----------------------------------
   if (tid == 0) {
     for (int i = 0; i < kBars; ++i) {
-      const uint32_t n = i == kBarK ? kDeqWarps
+      const uint32_t n = (i == kBarK || i == kBarV) ? kDeqWarps
                          : (i == kBarP0 || i == kBarP1) ? kSoftWarps
-                         : (i == kBarV0 || i == kBarV1) ? kDeqWarps / 2 : 1;
+                         : 1;
       asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar(i)), "r"(n) : "memory");
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -448,6 +453,7 @@ __device__ void shared_block(const SharedParams& p, unsigned char* sm, int unit)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");       // the tables are written
+  asm volatile("griddepcontrol.launch_dependents;");       // ... so the own grid may start
   if (tid == 0) request_tables(p, sm, hkv, bar(kBarTab));
   const int* exk = p.exps + hkv * 64;
   // the queries, scaled into fp16 (against the scales of the key groups): piece =
@@ -504,13 +510,14 @@ __device__ void shared_block(const SharedParams& p, unsigned char* sm, int unit)
   bool failed = false;                                     // this thread's wait gave up
   const int tok0 = tile0 * T::TOK;                         // first token of the split
 
-  if (warp >= kSoftWarps && warp < kSoftWarps + kDeqWarps) {
-    // ---- dequantisation ----------------------------------------------------------
+  if (warp >= kKWarp && warp < kMmaWarp) {
+    // ---- dequantisation: a team of eight warps per plane ------------------------------
+    if constexpr (N > 32) reg_dec<kDeqRegs>();
+    const bool values = warp >= kVWarp;
     const int blk = warp & 3, half = (warp >> 2) & 1;
     constexpr int W0 = (T::NW + 1) / 2;                    // index words of half 0 (half 1: the rest)
     const int w_first = half ? W0 : 0, w_n = half ? T::NW - W0 : W0;
     const int row = blk * 32 + lane;
-    const bool slot_ok = lane < T::LB;
     // per position: byte 0 its entry's place in a table row, bytes 2-3 its place
     // in a tile (below 32 KB)
     uint32_t at[4 * W0];
@@ -519,89 +526,73 @@ __device__ void shared_block(const SharedParams& p, unsigned char* sm, int unit)
       const int j = (w_first * 4 + w + lane) % J;
       at[w] = static_cast<uint32_t>(j * T::ENTRY) | (tile_off(row, j * T::ENTRY) << 16);
     }
-    const uint8_t* pool_h = p.pool_lg + hkv * p.pool_stride_head;
+    // this lane's row in block 0 of page 0 (granule of its first word)
+    const uint8_t* rows0 = p.pool_lg + hkv * p.pool_stride_head + (values ? p.plane_bytes : 0) + lane * T::GR +
+                           (J == 32 ? half * (T::LB * 16) : 0);
     const int32_t* bt = p.block_table + static_cast<int64_t>(lo) * p.max_pages_per_seq;
-    const int stage = blk >> 1;
-    // where this warp's block of tile i is: valid slots, and its address
-    auto entry_of = [&](int i) -> int {                    // page-table entry (warp-uniform), -1 past the end
-      const int b = (tile0 + i) * 4 + blk;
-      return (i < nt && b * T::LB < S) ? __ldg(bt + (b >> p.lbpp)) : -1;
-    };
-    auto load_rows = [&](int i, int entry, uint32_t (&kw)[W0], uint32_t (&vw)[W0]) -> int {
-      const int b = (tile0 + i) * 4 + blk;
-      int nv = i < nt ? max(0, min(T::LB, S - b * T::LB)) : 0;
-      if (nv > 0 && (entry < 0 || entry >= p.n_pages)) {
-        if (lane == 0 && p.status != nullptr) atomicOr(p.status, LOOPVQ_DECODE_STATUS_BAD_PAGE);
-        nv = 0;
+    const int blk0 = tile0 * 4 + blk;                      // this warp's block of tile i: blk0 + 4 i
+    // page-table entries of this warp's blocks of tiles e0 .. e0 + 31 (lane = tile)
+    int e0 = 0, entry;
+    auto load_entries = [&]() {
+      const int b = blk0 + (e0 + lane) * 4;
+      entry = e0 + lane < nt && b * T::LB < S ? __ldg(bt + (b >> p.lbpp)) : 0;
+      if (entry < 0 || entry >= p.n_pages) {
+        if (p.status != nullptr) atomicOr(p.status, LOOPVQ_DECODE_STATUS_BAD_PAGE);
+        entry = -1;
       }
+    };
+    load_entries();
+    // the index words of tile i, and the slots that hold a token
+    auto load_rows = [&](int i, uint32_t (&w)[W0]) -> int {
+      if (i >= e0 + 32) {                                  // warp-uniform
+        e0 += 32;
+        load_entries();
+      }
+      const int b = blk0 + i * 4, e = __shfl_sync(0xffffffffu, entry, i & 31);
+      const int nv = i < nt && e >= 0 ? min(T::LB, S - b * T::LB) : 0;   // <= 0: none
 #pragma unroll
-      for (int w = 0; w < W0; ++w) kw[w] = vw[w] = 0u;
-      if (nv > 0 && slot_ok) {
-        const uint8_t* r = pool_h + static_cast<int64_t>(entry) * p.page_bytes + (b & ((1 << p.lbpp) - 1)) * (T::LB * J) + lane * T::GR;
+      for (int k = 0; k < W0; ++k) w[k] = 0u;
+      if (nv > 0 && lane < T::LB) {
+        const uint8_t* r = rows0 + static_cast<int64_t>(e) * p.page_bytes + (b & ((1 << p.lbpp) - 1)) * (T::LB * J);
         if constexpr (J == 32) {
-          const uint4 k4 = __ldcs(reinterpret_cast<const uint4*>(r + half * (T::LB * 16)));
-          const uint4 v4 = __ldcs(reinterpret_cast<const uint4*>(r + half * (T::LB * 16) + p.plane_bytes));
-          kw[0] = k4.x; kw[1] = k4.y; kw[2] = k4.z; kw[3] = k4.w;
-          vw[0] = v4.x; vw[1] = v4.y; vw[2] = v4.z; vw[3] = v4.w;
+          const uint4 t = __ldcs(reinterpret_cast<const uint4*>(r));
+          w[0] = t.x; w[1] = t.y; w[2] = t.z; w[3] = t.w;
         } else {
 #pragma unroll
-          for (int w = 0; w < W0; ++w) {
-            if (w < w_n) {
-              const int byte = (w_first + w) * 4;
-              const uint8_t* a = r + byte / T::GR * (T::LB * T::GR) + byte % T::GR;
-              kw[w] = __ldcs(reinterpret_cast<const uint32_t*>(a));
-              vw[w] = __ldcs(reinterpret_cast<const uint32_t*>(a + p.plane_bytes));
-            }
+          for (int k = 0; k < W0; ++k) {
+            const int byte = (w_first + k) * 4;
+            if (k < w_n) w[k] = __ldcs(reinterpret_cast<const uint32_t*>(r + byte / T::GR * (T::LB * T::GR) + byte % T::GR));
           }
         }
       }
       return nv;
     };
-    // K runs one tile ahead of V: while the softmax of tile i is under way its
-    // scores' successor is already on the tensor cores
-    uint32_t kw[W0], vw[W0], vn[W0];                       // K rows of tile i + 1, V rows of tiles i and i + 1
-    auto fill_k = [&](int i, int nv) {
-      fill_block<J, C, kKtabOff, kKtileOff, W0>(kw, at, w_n, nv, lane);
-      if (half == 0 && lane == 0) nvs[(i & 3) * 4 + blk] = nv;
+    uint32_t w0[W0], w1[W0];                               // tiles i and i + 1
+    int nv0 = load_rows(0, w0), nv1 = load_rows(1, w1);
+    failed = !mbar_wait(bar(kBarTab), 0, kShSpin);
+#pragma unroll 1
+    for (int i = 0; i < nt; ++i) {
+      // the tile is free when S^T (K) or O^T (V) of the tile before is done
+      if (i > 0)
+        failed = !mbar_wait(bar((values ? kBarO0 : kBarS0) + ((i - 1) & 1)), ((i - 1) >> 1) & 1, kShSpin);
+      if (__any_sync(0xffffffffu, failed)) {
+        failed = true;
+        break;
+      }
+      if (values) {
+        fill_block<J, C, kVtabOff, kVtileOff, W0>(w0, at, w_n, nv0, lane);
+      } else {
+        fill_block<J, C, kKtabOff, kKtileOff, W0>(w0, at, w_n, nv0, lane);
+        if (half == 0 && lane == 0) nvs[(i & 3) * 4 + blk] = nv0;
+      }
       proxy_fence();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarK));
-    };
-    int e_next = entry_of(0);
-    int nv = load_rows(0, e_next, kw, vw);
-    e_next = entry_of(1);
-    failed = !mbar_wait(bar(kBarTab), 0, kShSpin);
-    if (!__any_sync(0xffffffffu, failed)) {
-      fill_k(0, nv);
-      int nv_next = load_rows(1, e_next, kw, vn);
-      e_next = entry_of(2);
-#pragma unroll 1
-      for (int i = 0; i < nt; ++i) {
-        uint32_t kl[W0], vl[W0];
-        const int nv_last = load_rows(i + 2, e_next, kl, vl);   // lands while this tile is filled
-        e_next = entry_of(i + 3);
-        if (i + 1 < nt) {
-          failed = !mbar_wait(bar(kBarS0 + (i & 1)), (i >> 1) & 1, kShSpin);
-          if (__any_sync(0xffffffffu, failed)) break;
-          fill_k(i + 1, nv_next);
-        }
-        if (i > 0) failed = !mbar_wait(bar(kBarVfree0 + stage), (i - 1) & 1, kShSpin);
-        if (__any_sync(0xffffffffu, failed)) break;
-        fill_block<J, C, kVtabOff, kVtileOff, W0>(vw, at, w_n, nv, lane);
-        proxy_fence();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarV0 + stage));
+      if (lane == 0) mbar_arrive(bar(values ? kBarV : kBarK));
 #pragma unroll
-        for (int w = 0; w < W0; ++w) {
-          kw[w] = kl[w];
-          vw[w] = vn[w];
-          vn[w] = vl[w];
-        }
-        nv = nv_next;
-        nv_next = nv_last;
-      }
+      for (int k = 0; k < W0; ++k) w0[k] = w1[k];
+      nv0 = nv1;
+      nv1 = load_rows(i + 2, w1);                          // lands during the next tile
     }
-    failed = __any_sync(0xffffffffu, failed);
   } else if (warp == kMmaWarp) {
     // ---- the products --------------------------------------------------------------
     if (lane == 0) {
@@ -611,46 +602,42 @@ __device__ void shared_block(const SharedParams& p, unsigned char* sm, int unit)
       const uint32_t p_hi = desc_hi(PP * 8, PP == 128 ? kSw128 : kSw64);
       const uint32_t k_lo = desc_lo(u32s(sm + kKtileOff), 16), q_lo = desc_lo(u32s(sm + kQOff), 16);
       const uint32_t v_lo = desc_lo(u32s(sm + kVtileOff), 1024), p_lo = desc_lo(u32s(sm + kPOff), 16);
-      int ns = 0, no = 0, spin = 0;                        // next scores, next output
+      auto product_s = [&](int i) {                        // S^T of tile i
+        tc_after();
+        const uint32_t d = tmem + kTmS + (i & 1) * 64;
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s)
+          tc_mma_f16_words(d, k_lo + ((s >> 2) * 1024 + (s & 3) * 32) / 16, k_hi,
+                           q_lo + ((s >> 2) * (N * 128) + (s & 3) * 32) / 16, q_hi, idesc_f16(N, 0, 0), s > 0 ? 1u : 0u);
+        tc_commit(bar(kBarS0 + (i & 1)));
+      };
+      // The keys run a tile ahead, so S^T of tile i + 1 is issued before O^T of
+      // tile i; its buffer is free since P of tile i - 1 was waited for.
+      failed = !mbar_wait(bar(kBarK), 0, kShSpin);
+      if (!failed) product_s(0);
 #pragma unroll 1
-      while (no < nt && !failed) {
-        bool idle = true;
-        // S^T of tile ns: its buffer is free once P of tile ns - 2 is written
-        if (ns < nt && ns <= no + 1 && mbar_test(bar(kBarK), ns & 1)) {
-          tc_after();
-          const uint32_t d = tmem + kTmS + (ns & 1) * 64;
-#pragma unroll
-          for (int s = 0; s < D / 16; ++s)
-            tc_mma_f16_words(d, k_lo + ((s >> 2) * 1024 + (s & 3) * 32) / 16, k_hi,
-                             q_lo + ((s >> 2) * (N * 128) + (s & 3) * 32) / 16, q_hi, idesc_f16(N, 0, 0), s > 0 ? 1u : 0u);
-          tc_commit(bar(kBarS0 + (ns & 1)));
-          ++ns;
-          idle = false;
+      for (int i = 0; i < nt && !failed; ++i) {
+        if (i + 1 < nt) {
+          failed = !mbar_wait(bar(kBarK), (i + 1) & 1, kShSpin);
+          if (failed) break;
+          product_s(i + 1);
         }
-        // O^T += V^T P of tile no
-        if (no < ns && mbar_test(bar(kBarP0 + no % PB), (no / PB) & 1) && mbar_test(bar(kBarV0), no & 1) &&
-            mbar_test(bar(kBarV1), no & 1)) {
-          tc_after();
-          const uint32_t pb = p_lo + (no % PB) * (kTileRows * PP) / 16;
+        failed = !mbar_wait(bar(kBarP0 + i % PB), (i / PB) & 1, kShSpin) || !mbar_wait(bar(kBarV), i & 1, kShSpin);
+        if (failed) break;
+        tc_after();
+        const uint32_t pb = p_lo + (i % PB) * (kTileRows * PP) / 16;
 #pragma unroll
-          for (int s = 0; s < 8; ++s) {
-            tc_mma_f16_words(tmem + kTmO, v_lo + s * 4096 / 16, v_hi, pb + s * (16 * PP) / 16, p_hi, idesc_f16(N, 1, 1),
-                             (no > 0 || s > 0) ? 1u : 0u);
-            if (s == 3) tc_commit(bar(kBarVfree0));
-          }
-          tc_commit(bar(kBarVfree1));
-          tc_commit(bar(kBarO0 + (no & 1)));
-          ++no;
-          idle = false;
-        }
-        spin = idle ? spin + 1 : 0;
-        failed = spin >= kShSpin;
+        for (int s = 0; s < 8; ++s)                        // O^T += V^T P, 16 tokens at a time
+          tc_mma_f16_words(tmem + kTmO, v_lo + s * 4096 / 16, v_hi, pb + s * (16 * PP) / 16, p_hi, idesc_f16(N, 1, 1),
+                           (i > 0 || s > 0) ? 1u : 0u);
+        tc_commit(bar(kBarO0 + (i & 1)));
       }
       tc_commit(bar(kBarDrain));                           // everything issued so far
     }
     __syncwarp();
   } else {
     // ---- softmax -------------------------------------------------------------------
+    if constexpr (N > 32) reg_inc<kSoftRegs>();
     const int quad = warp & 3, half = warp >> 2, row = quad * 32 + lane, c0 = half * NC;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const int bar_id = 1 + half;                           // the four warps of a column half
@@ -658,6 +645,9 @@ __device__ void shared_block(const SharedParams& p, unsigned char* sm, int unit)
 #pragma unroll
     for (int c = 0; c < NC; ++c) l[c] = 0.f;
     int mb = 0;
+    float4 m4[NC / 4];                                     // this half's references
+#pragma unroll
+    for (int c = 0; c < NC / 4; ++c) m4[c] = make_float4(kUnset, kUnset, kUnset, kUnset);
 #pragma unroll 1
     for (int i = 0; i < nt; ++i) {
       failed = !mbar_wait(bar(kBarS0 + (i & 1)), (i >> 1) & 1, kShSpin);
@@ -667,9 +657,6 @@ __device__ void shared_block(const SharedParams& p, unsigned char* sm, int unit)
       tld<NC>(lanes + kTmS + (i & 1) * 64 + c0, sv);
       const int nv = nvs[(i & 3) * 4 + quad];
       const float* m = m_ref + mb * kMaxRows + c0;
-      float4 m4[NC / 4];
-#pragma unroll
-      for (int c = 0; c < NC / 4; ++c) m4[c] = *reinterpret_cast<const float4*>(m + 4 * c);
       tld_wait();
       if (nv < 32 && lane >= nv) {                         // no token in this slot
 #pragma unroll
@@ -684,10 +671,10 @@ __device__ void shared_block(const SharedParams& p, unsigned char* sm, int unit)
       float mx = -INFINITY;
 #pragma unroll
       for (int c = 0; c < NC; c += 4) {
-        mx = fmaxf(mx, fmaxf(fmaf(__uint_as_float(sv[c]), scale, -m4[c / 4].x),
-                             fmaf(__uint_as_float(sv[c + 1]), scale, -m4[c / 4].y)));
-        mx = fmaxf(mx, fmaxf(fmaf(__uint_as_float(sv[c + 2]), scale, -m4[c / 4].z),
-                             fmaf(__uint_as_float(sv[c + 3]), scale, -m4[c / 4].w)));
+        const float4 mm = m4[c / 4];
+        mx = fmaxf(mx, fmaxf(fmaf(__uint_as_float(sv[c]), scale, -mm.x), fmaf(__uint_as_float(sv[c + 1]), scale, -mm.y)));
+        mx = fmaxf(mx, fmaxf(fmaf(__uint_as_float(sv[c + 2]), scale, -mm.z),
+                             fmaf(__uint_as_float(sv[c + 3]), scale, -mm.w)));
       }
       if (i >= PB) failed = !mbar_wait(bar(kBarO0 + ((i - PB) & 1)), ((i - PB) >> 1) & 1, kShSpin) || failed;
       if (named_or(bar_id, 128, mx > kRaise || failed)) {
@@ -741,13 +728,18 @@ __device__ void shared_block(const SharedParams& p, unsigned char* sm, int unit)
       for (int c = 0; c < NC; c += 8) {
         uint32_t w[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 4; k += 2) {
           const float4 mm = m4[(c + 2 * k) / 4];
-          const float a = fast_exp2(fmaf(__uint_as_float(sv[c + 2 * k]), scale, -((k & 1) ? mm.z : mm.x)));
-          const float b = fast_exp2(fmaf(__uint_as_float(sv[c + 2 * k + 1]), scale, -((k & 1) ? mm.w : mm.y)));
-          l[c + 2 * k] += a;
-          l[c + 2 * k + 1] += b;
-          w[k] = half2_bits(a, b);
+          const float e0 = fast_exp2(fmaf(__uint_as_float(sv[c + 2 * k]), scale, -mm.x));
+          const float e1 = fast_exp2(fmaf(__uint_as_float(sv[c + 2 * k + 1]), scale, -mm.y));
+          const float e2 = fast_exp2(fmaf(__uint_as_float(sv[c + 2 * k + 2]), scale, -mm.z));
+          const float e3 = fast_exp2(fmaf(__uint_as_float(sv[c + 2 * k + 3]), scale, -mm.w));
+          l[c + 2 * k] += e0;
+          l[c + 2 * k + 1] += e1;
+          l[c + 2 * k + 2] += e2;
+          l[c + 2 * k + 3] += e3;
+          w[k] = half2_bits(e0, e1);
+          w[k + 1] = half2_bits(e2, e3);
         }
         *reinterpret_cast<uint4*>(prow + ((((c0 + c) >> 3) ^ swz) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
       }
@@ -823,7 +815,10 @@ constexpr int kOwnRows = 0;
 constexpr int kOwnQ = 32 * kOwnPitch;
 constexpr int kOwnP = kOwnQ + 1536;
 constexpr int kOwnBytes = kOwnP + 128;
-static_assert(kShWarps * kOwnBytes <= kMOff - kKtileOff, "own scratch fits the tile area");
+constexpr int kOwnWarps = 16;
+constexpr int kOwnBarOff = kKtileOff + kOwnWarps * kOwnBytes;
+constexpr int kOwnSmem = kOwnBarOff + 16;
+static_assert(kOwnSmem <= 227 * 1024, "shared memory above 227 KB");
 
 // Softmax state of one warp: m in log2 units; lane = (side, channel group j)
 // holds the o of group j over its side's tokens; l per lane (any share).
@@ -1077,19 +1072,26 @@ __device__ void own_chunk(const SharedParams& p, const uint8_t* pool_h, int b, i
   own_record<J, C>(s, unscale, rec, lane);
 }
 
+// Runs beside the shared grid, on the SMs that it leaves free: the shared blocks
+// start this grid once the tables are written.
 template <int J, int C>
-__device__ void own_block(const SharedParams& p, unsigned char* sm, int unit) {
+__global__ void __launch_bounds__(kOwnWarps * 32, 1) shared_own_kernel(const SharedParams p) {
   using T = Shape<J, C>;
   constexpr int D = T::D;
+  extern __shared__ __align__(1024) unsigned char sm[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int hkv = unit % p.Hkv, part = unit / p.Hkv;
-  const uint32_t bar = u32s(sm + kBarOff);
+  const int hkv = blockIdx.x % p.Hkv, part = blockIdx.x / p.Hkv;
+  const uint32_t bar = u32s(sm + kOwnBarOff);
+  if (u32s(sm) != kShBase) {                               // the host checks this before launching
+    if (tid == 0 && p.status != nullptr) atomicOr(p.status, LOOPVQ_DECODE_STATUS_SHARED_BASE);
+    return;
+  }
   if (tid == 0) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(1u) : "memory");
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
-  asm volatile("griddepcontrol.wait;" ::: "memory");       // the tables are written
+  if (p.shared_blocks == 0) asm volatile("griddepcontrol.wait;" ::: "memory");   // this grid follows the tables' own
   if (tid == 0) request_tables(p, sm, hkv, bar);
   const bool failed = __syncthreads_or(!mbar_wait(bar, 0, kShSpin));
   if (failed && tid == 0) {                                // no copy may outlive the block
@@ -1104,8 +1106,8 @@ __device__ void own_block(const SharedParams& p, unsigned char* sm, int unit) {
   float* qs = reinterpret_cast<float*>(scratch + kOwnQ);
   const uint8_t* pool_h = p.pool_lg + hkv * p.pool_stride_head;
   const int64_t tasks = static_cast<int64_t>(p.B) * p.ratio * p.NC;
-  for (int64_t t = static_cast<int64_t>(part) * kShWarps + warp; t < tasks;
-       t += static_cast<int64_t>(p.own_parts) * kShWarps) {
+  for (int64_t t = static_cast<int64_t>(part) * kOwnWarps + warp; t < tasks;
+       t += static_cast<int64_t>(p.own_parts) * kOwnWarps) {
     const int ck = static_cast<int>(t % p.NC) - 1;         // -1: the window
     const int64_t y = t / p.NC;
     const int r = static_cast<int>(y % p.ratio), b = static_cast<int>(y / p.ratio);
@@ -1141,26 +1143,25 @@ __device__ void own_block(const SharedParams& p, unsigned char* sm, int unit) {
     __syncwarp();
     own_chunk<J, C>(p, pool_h, b, t0, t1, unv, scratch, rec, lane);
   }
+  // the merge waits for this grid, which ends after the shared one
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 template <int J, int C, int N>
-__global__ void __launch_bounds__(kShThreads, 1) shared_attn_kernel(const SharedParams p) {
+__global__ void __launch_bounds__(kShThreads, 1) shared_prefix_kernel(const SharedParams p) {
   extern __shared__ __align__(1024) unsigned char sm[];
-  if (u32s(sm) != kShBase) {                          // the host checks this before launching
+  if (u32s(sm) != kShBase) {                               // the host checks this before launching
     if (threadIdx.x == 0 && p.status != nullptr) atomicOr(p.status, LOOPVQ_DECODE_STATUS_SHARED_BASE);
     return;
   }
-  const int unit = blockIdx.x;
-  if (unit < p.shared_blocks)
-    shared_block<J, C, N>(p, sm, unit);
-  else
-    own_block<J, C>(p, sm, unit - p.shared_blocks);
+  shared_block<J, C, N>(p, sm, blockIdx.x);
 }
 
 // One warp per (sequence, query head): joins the records that its blocks wrote.
 template <int D>
 __global__ void __launch_bounds__(128) shared_merge_kernel(const SharedParams p) {
   constexpr int RS = 4 + D, NCH = (D + 31) / 32;
+  asm volatile("griddepcontrol.wait;" ::: "memory");       // every record is written
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t pair = static_cast<int64_t>(blockIdx.x) * 4 + warp;
   if (pair >= static_cast<int64_t>(p.B) * p.Hq) return;
@@ -1234,10 +1235,10 @@ SharedPlan make_plan(const Geometry& g, int batch, int n_groups, int max_group, 
   const int64_t tasks = static_cast<int64_t>(batch) * ratio * q.NC;      // warps' tasks of one head
   // rough block times (cycles): setup, a tile, a task of a whole chunk
   const double setup = 6000, t_tile = 1800, t_task = 6000;
-  const double work_a = units * (tiles * t_tile), work_b = g.Hkv * (tasks * t_task / kShWarps);
+  const double work_a = units * (tiles * t_tile), work_b = g.Hkv * (tasks * t_task / kOwnWarps);
   int parts = static_cast<int>(kPlanSms / g.Hkv * work_b / (work_a + work_b + 1) + 0.5);
   if (parts < 1) parts = 1;
-  const int64_t most = (tasks + kShWarps - 1) / kShWarps;
+  const int64_t most = (tasks + kOwnWarps - 1) / kOwnWarps;
   int64_t room = kPlanSms - static_cast<int64_t>(parts) * g.Hkv;
   q.NS = 1;
   if (units > 0) {
@@ -1263,33 +1264,33 @@ SharedPlan make_plan(const Geometry& g, int batch, int n_groups, int max_group, 
   return q;
 }
 
-template <int J, int C, int N>
-loopvq_status launch_shared_n(const SharedParams& p, cudaStream_t st) {
-  static std::atomic<uint64_t> configured{0};
+// Gives `kernel` its dynamic shared memory on this device (once), after
+// checking that the allocation starts where the kernels' addresses need it.
+template <typename K>
+loopvq_status configure(K kernel, int smem, std::atomic<uint64_t>& configured) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return LOOPVQ_ERR_CUDA;
   const uint64_t bit = (dev >= 0 && dev < 64) ? (1ull << dev) : 0ull;
-  auto kernel = shared_attn_kernel<J, C, N>;
-  if (bit == 0 || !(configured.load(std::memory_order_relaxed) & bit)) {
-    int reserved = -1;
-    if (cudaDeviceGetAttribute(&reserved, cudaDevAttrReservedSharedMemoryPerBlock, dev) != cudaSuccess)
-      return LOOPVQ_ERR_CUDA;
-    cudaFuncAttributes fa{};
-    if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess) return LOOPVQ_ERR_CUDA;
-    if (reserved != static_cast<int>(kShBase) || fa.sharedSizeBytes != 0) return LOOPVQ_ERR_UNSUPPORTED;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kShSmem) != cudaSuccess)
-      return LOOPVQ_ERR_CUDA;
-    configured.fetch_or(bit, std::memory_order_relaxed);
-  }
-  const int64_t blocks = static_cast<int64_t>(p.shared_blocks) + static_cast<int64_t>(p.Hkv) * p.own_parts;
-  shared_table_kernel<J, C><<<dim3(J / 4, 2, p.Hkv), kE, 0, st>>>(p.cb_k, p.cb_v, p.cb_stride_head,
-                                                                  const_cast<unsigned char*>(p.tables),
-                                                                  const_cast<int*>(p.exps));
-  if (cudaGetLastError() != cudaSuccess) return LOOPVQ_ERR_CUDA;
+  if (bit != 0 && (configured.load(std::memory_order_relaxed) & bit)) return LOOPVQ_OK;
+  int reserved = -1;
+  if (cudaDeviceGetAttribute(&reserved, cudaDevAttrReservedSharedMemoryPerBlock, dev) != cudaSuccess)
+    return LOOPVQ_ERR_CUDA;
+  cudaFuncAttributes fa{};
+  if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess) return LOOPVQ_ERR_CUDA;
+  if (reserved != static_cast<int>(kShBase) || fa.sharedSizeBytes != 0) return LOOPVQ_ERR_UNSUPPORTED;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return LOOPVQ_ERR_CUDA;
+  configured.fetch_or(bit, std::memory_order_relaxed);
+  return LOOPVQ_OK;
+}
+
+// Launches `kernel` as a programmatic dependent of the kernel before it.
+template <typename K>
+loopvq_status launch_after(K kernel, int64_t blocks, int threads, int smem, cudaStream_t st, const SharedParams& p) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-  cfg.blockDim = dim3(kShThreads);
-  cfg.dynamicSmemBytes = kShSmem;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1297,19 +1298,34 @@ loopvq_status launch_shared_n(const SharedParams& p, cudaStream_t st) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) return LOOPVQ_ERR_CUDA;
-  if (cudaGetLastError() != cudaSuccess) return LOOPVQ_ERR_CUDA;
-  const int64_t pairs = static_cast<int64_t>(p.B) * p.Hq;
-  shared_merge_kernel<J * C><<<static_cast<unsigned>((pairs + 3) / 4), 128, 0, st>>>(p);
   return cudaGetLastError() == cudaSuccess ? LOOPVQ_OK : LOOPVQ_ERR_CUDA;
+}
+
+template <int J, int C, int N>
+loopvq_status launch_prefix(const SharedParams& p, cudaStream_t st) {
+  static std::atomic<uint64_t> configured{0};
+  const loopvq_status s = configure(shared_prefix_kernel<J, C, N>, kShSmem, configured);
+  if (s != LOOPVQ_OK) return s;
+  return launch_after(shared_prefix_kernel<J, C, N>, p.shared_blocks, kShThreads, kShSmem, st, p);
 }
 
 template <int J, int C>
 loopvq_status launch_shared_jc(const SharedParams& p, int N, cudaStream_t st) {
-  switch (N) {
-    case 16: return launch_shared_n<J, C, 16>(p, st);
-    case 32: return launch_shared_n<J, C, 32>(p, st);
-    default: return launch_shared_n<J, C, 64>(p, st);
+  static std::atomic<uint64_t> configured{0};
+  loopvq_status s = configure(shared_own_kernel<J, C>, kOwnSmem, configured);
+  if (s != LOOPVQ_OK) return s;
+  shared_table_kernel<J, C><<<dim3(J / 4, 2, p.Hkv), kE, 0, st>>>(p.cb_k, p.cb_v, p.cb_stride_head,
+                                                                  const_cast<unsigned char*>(p.tables),
+                                                                  const_cast<int*>(p.exps));
+  if (cudaGetLastError() != cudaSuccess) return LOOPVQ_ERR_CUDA;
+  if (p.shared_blocks > 0) {
+    s = N == 16 ? launch_prefix<J, C, 16>(p, st) : N == 32 ? launch_prefix<J, C, 32>(p, st) : launch_prefix<J, C, 64>(p, st);
+    if (s != LOOPVQ_OK) return s;
   }
+  s = launch_after(shared_own_kernel<J, C>, static_cast<int64_t>(p.Hkv) * p.own_parts, kOwnWarps * 32, kOwnSmem, st, p);
+  if (s != LOOPVQ_OK) return s;
+  const int64_t pairs = static_cast<int64_t>(p.B) * p.Hq;
+  return launch_after(shared_merge_kernel<J * C>, (pairs + 3) / 4, 128, 0, st, p);
 }
 
 size_t record_bytes(const Geometry& g, int batch, int slots) {
