@@ -121,6 +121,7 @@ struct SharedParams {
   const uint16_t* win_v;
   const unsigned char* tables;    // [Hkv][K, V] fp16 tables of kTabBytes
   const int* exps;                // [Hkv][K, V][32]: a group's table entries are scaled by 2^exps
+  int2* seqs;                     // [B] shared and own quantised tokens of a sequence
   float* srec;                    // [pairs][NS][4 + d] records of the shared blocks
   float* orec;                    // [pairs][NC][4 + d] records of the own chunks
   int* status;
@@ -202,10 +203,6 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ float2 half2_floats(uint32_t w) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&w));
-}
-
 // NC columns of this warp's 32 TMEM lanes.
 template <int NC>
 __device__ __forceinline__ void tld(uint32_t a, uint32_t (&r)[NC]) {
@@ -280,14 +277,50 @@ __device__ __forceinline__ float finite_abs(float v) {
   return a < INFINITY ? a : 0.f;
 }
 
+// Quantised tokens of sequence b.
+__device__ __forceinline__ int seq_vq(const SharedParams& p, int b) {
+  return max(0, min(__ldg(p.seq_lens + b) - p.W, p.max_pages_per_seq * p.Pg));
+}
+
+// Group of sequence b (-1: none); every lane of the warp calls it.
+__device__ __forceinline__ int group_of(const SharedParams& p, int b, int lane) {
+  int n = 0;
+  for (int i = lane; i < p.n_groups; i += 32) n += __ldg(p.group_starts + 1 + i) <= b ? 1 : 0;
+  const int g = __reduce_add_sync(0xffffffffu, n);
+  if (g >= p.n_groups || b < __ldg(p.group_starts + g) || b >= __ldg(p.group_starts + g + 1)) return -1;
+  if (b - __ldg(p.group_starts + g) >= p.max_group) return -1;
+  return g;
+}
+__device__ __forceinline__ int group_shared(const SharedParams& p, int g) {
+  return max(0, min(__ldg(p.shared_lens + g), p.max_shared));
+}
+
 // The codebook slices of one call as fp16 tables: block (4 channel groups, K or
 // V, head), thread = codeword. Each group is scaled by a power of two of its
-// own. Blocks of the attention grid start meanwhile and wait for this grid.
+// own. Also the split of every sequence into shared and own tokens. Blocks of the
+// attention grid start meanwhile and wait for this grid.
 template <int J, int C>
 __global__ void __launch_bounds__(kE) shared_table_kernel(const float* cb_k, const float* cb_v, int64_t cb_stride_head,
-                                                          unsigned char* tables, int* exps) {
+                                                          unsigned char* tables, int* exps, const SharedParams p) {
   __shared__ float red[4][kE / 32];
   asm volatile("griddepcontrol.launch_dependents;");
+  {                                                        // a warp per sequence: its shared and own tokens
+    const int lane = threadIdx.x & 31, blocks = gridDim.x * gridDim.y * gridDim.z;
+    const int id = (blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
+    for (int g = id * kE + static_cast<int>(threadIdx.x); g < p.n_groups; g += blocks * kE) {
+      const int lo = __ldg(p.group_starts + g), hi = __ldg(p.group_starts + g + 1), s = __ldg(p.shared_lens + g);
+      if ((lo < 0 || hi > p.B || hi < lo || hi - lo > p.max_group || s < 0 || s > p.max_shared) && p.status != nullptr)
+        atomicOr(p.status, LOOPVQ_DECODE_STATUS_BAD_GROUP);
+    }
+    for (int b = id + static_cast<int>(threadIdx.x >> 5) * blocks; b < p.B; b += blocks * (kE / 32)) {
+      const int n_vq = seq_vq(p, b), g = group_of(p, b, lane);
+      const int s0 = g < 0 ? 0 : min(group_shared(p, g), n_vq), n_own = min(n_vq - s0, p.max_own);
+      if (lane == 0) {
+        p.seqs[b] = make_int2(s0, n_own);
+        if (n_own < n_vq - s0 && p.status != nullptr) atomicOr(p.status, LOOPVQ_DECODE_STATUS_BAD_GROUP);
+      }
+    }
+  }
   const int j0 = blockIdx.x * 4, kv = blockIdx.y, h = blockIdx.z, e = threadIdx.x;
   const float* cb = (kv ? cb_v : cb_k) + h * cb_stride_head;
   float4 v[4][C / 4];
@@ -335,24 +368,6 @@ __device__ __forceinline__ void request_tables(const SharedParams& p, unsigned c
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                      u32s(sm + kKtabOff + part * (kTabBytes / 2))),
                  "l"(src + part * (kTabBytes / 2)), "r"(kTabBytes / 2), "r"(bar) : "memory");
-}
-
-// Quantised tokens of sequence b.
-__device__ __forceinline__ int seq_vq(const SharedParams& p, int b) {
-  return max(0, min(__ldg(p.seq_lens + b) - p.W, p.max_pages_per_seq * p.Pg));
-}
-
-// Group of sequence b (-1: none); every lane of the warp calls it.
-__device__ __forceinline__ int group_of(const SharedParams& p, int b, int lane) {
-  int n = 0;
-  for (int i = lane; i < p.n_groups; i += 32) n += __ldg(p.group_starts + 1 + i) <= b ? 1 : 0;
-  const int g = __reduce_add_sync(0xffffffffu, n);
-  if (g >= p.n_groups || b < __ldg(p.group_starts + g) || b >= __ldg(p.group_starts + g + 1)) return -1;
-  if (b - __ldg(p.group_starts + g) >= p.max_group) return -1;
-  return g;
-}
-__device__ __forceinline__ int group_shared(const SharedParams& p, int g) {
-  return max(0, min(__ldg(p.shared_lens + g), p.max_shared));
 }
 
 // Number of shared tiles of split s of T tiles over NS splits: [first, last).
@@ -411,11 +426,6 @@ __device__ void shared_block(const SharedParams& p, unsigned char* sm, int unit)
   x /= p.Hkv;
   const int rt = x % p.RT, g = x / p.RT;
   const int lo = max(0, __ldg(p.group_starts + g)), hi = min(p.B, __ldg(p.group_starts + g + 1));
-  if (split == 0 && hkv == 0 && rt == 0 && tid == 0 && p.status != nullptr) {
-    const int a = __ldg(p.group_starts + g), z = __ldg(p.group_starts + g + 1), s = __ldg(p.shared_lens + g);
-    if (a < 0 || z > p.B || z < a || z - a > p.max_group || s < 0 || s > p.max_shared)
-      atomicOr(p.status, LOOPVQ_DECODE_STATUS_BAD_GROUP);
-  }
   const int rows = min(max(0, min(hi - lo, p.max_group) * p.ratio - rt * N), N);   // this tile's query rows
   const int S = group_shared(p, g);
   const int tiles = (S + T::TOK - 1) / T::TOK;
@@ -806,160 +816,149 @@ __device__ void shared_block(const SharedParams& p, unsigned char* sm, int unit)
 
 // ---- own blocks ------------------------------------------------------------------
 
-// Per-warp scratch of an own block, in the tile area: value index rows (each
-// twice over, so that group j of slot k sits at byte J - k + j of its row), the
-// query twice over (so that lane i finds group (i + s) mod J at entry i + s), and
-// a block's softmax weights.
+// Per-warp scratch of an own block: value index rows (each twice over, so that
+// group j of slot k sits at byte J - k + j of its row), the query in fp16 twice
+// over (so that lane i finds group (i + s) mod J at entry i + s), and a block's
+// softmax weights in fp16.
 constexpr int kOwnPitch = 80;                              // bytes of an index row (conflict-free 16-byte stores)
 constexpr int kOwnRows = 0;
 constexpr int kOwnQ = 32 * kOwnPitch;
-constexpr int kOwnP = kOwnQ + 1536;
-constexpr int kOwnBytes = kOwnP + 128;
+constexpr int kOwnP = kOwnQ + 768;
+constexpr int kOwnBytes = kOwnP + 64;
 constexpr int kOwnWarps = 16;
-constexpr int kOwnBarOff = kKtileOff + kOwnWarps * kOwnBytes;
+constexpr int kOwnFkOff = 2 * kTabBytes;                   // float [32]: 2^-exps of the key groups
+constexpr int kOwnScratch = kOwnFkOff + 128;
+constexpr int kOwnBarOff = kOwnScratch + kOwnWarps * kOwnBytes;
 constexpr int kOwnSmem = kOwnBarOff + 16;
 static_assert(kOwnSmem <= 227 * 1024, "shared memory above 227 KB");
 
-// Softmax state of one warp: m in log2 units; lane = (side, channel group j)
-// holds the o of group j over its side's tokens; l per lane (any share).
-template <int C>
-struct OwnState {
-  float m, l, o[C];
-};
-// Takes the warp's new maximum mx in.
-template <int C>
-__device__ __forceinline__ void own_raise(OwnState<C>& s, float mx) {
-  if (mx > s.m) {                                          // warp-uniform
-    const float f = s.m == -INFINITY ? 0.f : fast_exp2(s.m - mx);
-    s.l *= f;
-#pragma unroll
-    for (int c = 0; c < C; ++c) s.o[c] *= f;
-    s.m = mx;
-  }
+// acc += a . b over the two fp16 of each word, products exact, float32 sums
+// (mixed-precision multiply-add: no conversion instructions).
+__device__ __forceinline__ void dot_f16(float& acc, uint32_t a, uint32_t b) {
+  asm("{\n .reg .b16 al, ah, bl, bh;\n mov.b32 {al, ah}, %1;\n mov.b32 {bl, bh}, %2;\n"
+      " fma.rn.f32.f16 %0, al, bl, %0;\n fma.rn.f32.f16 %0, ah, bh, %0;\n}\n" : "+f"(acc) : "r"(a), "r"(b));
+}
+// The same over two bf16.
+__device__ __forceinline__ void dot_bf16(float& acc, uint32_t a, uint32_t b) {
+  asm("{\n .reg .b16 al, ah, bl, bh;\n mov.b32 {al, ah}, %1;\n mov.b32 {bl, bh}, %2;\n"
+      " fma.rn.f32.bf16 %0, al, bl, %0;\n fma.rn.f32.bf16 %0, ah, bh, %0;\n}\n" : "+f"(acc) : "r"(a), "r"(b));
+}
+// (x, y) += w * v over the two fp16 of v; w the low (0) or high (1) fp16 of its word.
+template <int HIGH>
+__device__ __forceinline__ void axpy_f16(float& x, float& y, uint32_t w, uint32_t v) {
+  if constexpr (HIGH)
+    asm("{\n .reg .b16 wl, wh, vl, vh;\n mov.b32 {wl, wh}, %2;\n mov.b32 {vl, vh}, %3;\n"
+        " fma.rn.f32.f16 %0, wh, vl, %0;\n fma.rn.f32.f16 %1, wh, vh, %1;\n}\n" : "+f"(x), "+f"(y) : "r"(w), "r"(v));
+  else
+    asm("{\n .reg .b16 wl, wh, vl, vh;\n mov.b32 {wl, wh}, %2;\n mov.b32 {vl, vh}, %3;\n"
+        " fma.rn.f32.f16 %0, wl, vl, %0;\n fma.rn.f32.f16 %1, wl, vh, %1;\n}\n" : "+f"(x), "+f"(y) : "r"(w), "r"(v));
 }
 
-// The record of one task: sides joined, l summed over the warp.
-template <int J, int C>
-__device__ __forceinline__ void own_record(const OwnState<C>& s, float unscale, float* rec, int lane) {
-  constexpr int TPS = Shape<J, C>::TPS;
-  const float l = warp_sum(s.l);
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    float o = s.o[c];
-#pragma unroll
-    for (int k = 1; k < TPS; ++k) o += __shfl_sync(0xffffffffu, s.o[c], (lane + k * J) & 31);
-    if (lane < J) rec[4 + lane * C + c] = o * unscale;
-  }
-  if (lane == 0) {
-    rec[0] = l == l ? s.m : NAN;
-    rec[1] = l;
-  }
-}
-
-// bf16 window of (b, hkv): lane = C channels, 32/J tokens side by side, U steps
-// of loads ahead of the sums.
-template <int J, int C>
-__device__ void own_window(const SharedParams& p, int64_t head, int n_win, const float (&q)[C], float* rec, int lane) {
-  using T = Shape<J, C>;
-  constexpr int U = 8, D = T::D;
-  const int side = lane / J, j = lane % J;
-  const bool act = side < T::TPS;
-  OwnState<C> s;
-  s.m = -INFINITY;
-  s.l = 0.f;
-#pragma unroll
-  for (int c = 0; c < C; ++c) s.o[c] = 0.f;
-  const uint16_t* wk = p.win_k + head * p.W * D + j * C;
-  const uint16_t* wv = p.win_v + head * p.W * D + j * C;
-  uint32_t kr[U][C / 2], vr[U][C / 2];
+// bf16 window of (b, hkv): lane = 4 channels, D/4 lanes a token (two tokens side
+// by side at D = 64), eight steps of rows requested ahead of their sums. The
+// scores of eight tokens are summed over the lanes together, half of them
+// changing lanes at each of the first three exchanges.
+template <int D>
+__device__ void own_window(const SharedParams& p, int64_t head, int n_win, const uint16_t* qp, float* rec, int lane) {
+  constexpr int LN = D <= 64 ? 16 : 32, SIDES = 32 / LN, U = 8;
+  const int side = lane / LN, c4 = lane % LN;              // channels 4 c4 ..
+  const bool act = c4 * 4 < D;
+  const uint2 q = act ? *reinterpret_cast<const uint2*>(qp + 4 * c4) : make_uint2(0u, 0u);
+  const uint16_t* wk = p.win_k + head * p.W * D + 4 * c4;
+  const uint16_t* wv = p.win_v + head * p.W * D + 4 * c4;
+  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+  uint2 kr[U], vr[U];
   auto request = [&](int n0) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int n = n0 + u * T::TPS + side;
+      const int n = n0 + u * SIDES + side;
       const bool ok = act && n < n_win;
-#pragma unroll
-      for (int c = 0; c < C / 2; ++c) {
-        kr[u][c] = ok ? __ldg(reinterpret_cast<const uint32_t*>(wk + static_cast<int64_t>(n) * D) + c) : 0u;
-        vr[u][c] = ok ? __ldg(reinterpret_cast<const uint32_t*>(wv + static_cast<int64_t>(n) * D) + c) : 0u;
-      }
+      kr[u] = ok ? __ldg(reinterpret_cast<const uint2*>(wk + static_cast<int64_t>(n) * D)) : make_uint2(0u, 0u);
+      vr[u] = ok ? __ldg(reinterpret_cast<const uint2*>(wv + static_cast<int64_t>(n) * D)) : make_uint2(0u, 0u);
     }
   };
   request(0);
 #pragma unroll 1
-  for (int n0 = 0; n0 < n_win; n0 += U * T::TPS) {
+  for (int n0 = 0; n0 < n_win; n0 += U * SIDES) {
     float x[U];
+    uint2 v[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       x[u] = 0.f;
+      dot_bf16(x[u], q.x, kr[u].x);
+      dot_bf16(x[u], q.y, kr[u].y);
+      v[u] = vr[u];
+    }
+    if (n0 + U * SIDES < n_win) request(n0 + U * SIDES);
 #pragma unroll
-      for (int c = 0; c < C / 2; ++c) {
-        const float2 k = bf16x2_to_float2(kr[u][c]);
-        x[u] = fmaf(q[2 * c], k.x, fmaf(q[2 * c + 1], k.y, x[u]));
+    for (int h = U / 2, off = LN / 2; h >= 1; h >>= 1, off >>= 1) {
+      const bool up = (lane & off) != 0;
+#pragma unroll
+      for (int i = 0; i < h; ++i) {
+        const float give = up ? x[i] : x[i + h], keep = up ? x[i + h] : x[i];
+        x[i] = keep + __shfl_xor_sync(0xffffffffu, give, off);
       }
     }
-    uint32_t v[U][C / 2];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int off = LN / 16; off >= 1; off >>= 1) x[0] += __shfl_xor_sync(0xffffffffu, x[0], off);
+    // this lane's token: bits LN/2, LN/4, LN/8 of the lane are its number's
+    const int mine = ((lane & (LN / 2)) ? 4 : 0) | ((lane & (LN / 4)) ? 2 : 0) | ((lane & (LN / 8)) ? 1 : 0);
+    const float xm = n0 + mine * SIDES + side < n_win ? x[0] * p.scale_log2 : -INFINITY;
+    const float mx = redux_fmax(xm);
+    if (mx > m) {                                          // warp-uniform
+      const float f = m == -INFINITY ? 0.f : fast_exp2(m - mx);
+      l *= f;
 #pragma unroll
-      for (int c = 0; c < C / 2; ++c) v[u][c] = vr[u][c];
-    if (n0 + U * T::TPS < n_win) request(n0 + U * T::TPS);
-    float mx = -INFINITY;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {                          // sum over the side's J lanes
-      if constexpr ((J & (J - 1)) == 0) {
-#pragma unroll
-        for (int o = J / 2; o > 0; o >>= 1) x[u] += __shfl_xor_sync(0xffffffffu, x[u], o);
-      } else {
-        const int base = min(side, T::TPS - 1) * J;
-        float t = 0.f;
-#pragma unroll
-        for (int k = 0; k < J; ++k) t += __shfl_sync(0xffffffffu, x[u], base + k);
-        x[u] = t;
-      }
-      if (!act || n0 + u * T::TPS + side >= n_win) x[u] = -INFINITY;
-      mx = fmaxf(mx, x[u]);
+      for (int c = 0; c < 4; ++c) o[c] *= f;
+      m = mx;
     }
-    own_raise<C>(s, redux_fmax(mx));
-    const float ref = s.m == -INFINITY ? 0.f : s.m;
+    const float w = fast_exp2(xm - (m == -INFINITY ? 0.f : m));
+    if ((lane & (LN / 8 - 1)) == 0) l += w;                // one lane counts a token
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const float w = fast_exp2(x[u] - ref);
-      if (j == 0) s.l += w;                                // one lane of the side counts it
-#pragma unroll
-      for (int c = 0; c < C / 2; ++c) {
-        const float2 f = bf16x2_to_float2(v[u][c]);
-        s.o[2 * c] = fmaf(w, f.x, s.o[2 * c]);
-        s.o[2 * c + 1] = fmaf(w, f.y, s.o[2 * c + 1]);
-      }
+      const float wu = __shfl_sync(0xffffffffu, w, side * LN + ((u & 4) ? LN / 2 : 0) + ((u & 2) ? LN / 4 : 0) + ((u & 1) ? LN / 8 : 0));
+      const float2 a = bf16x2_to_float2(v[u].x), b = bf16x2_to_float2(v[u].y);
+      o[0] = fmaf(wu, a.x, o[0]);
+      o[1] = fmaf(wu, a.y, o[1]);
+      o[2] = fmaf(wu, b.x, o[2]);
+      o[3] = fmaf(wu, b.y, o[3]);
     }
   }
-  own_record<J, C>(s, 1.f, rec, lane);
+  l = warp_sum(l);
+  if constexpr (SIDES == 2) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) o[c] += __shfl_xor_sync(0xffffffffu, o[c], 16);
+  }
+  if (act && side == 0) *reinterpret_cast<float4*>(rec + 4 + 4 * c4) = make_float4(o[0], o[1], o[2], o[3]);
+  if (lane == 0) {
+    rec[0] = l == l ? m : NAN;
+    rec[1] = l;
+  }
 }
 
 // Quantised tokens [t0, t1) of sequence b, a block of LB slots at a time.
 // Scores: lane = slot, byte s of its rotated key row is group (slot + s) mod J,
 // its codeword and the query's channels of that group come from shared memory
 // without bank conflicts. Values: lane = (side, group j), token by token.
+// Weights are 2^(x - m) with m 14 below the running maximum, so that their fp16
+// copies keep full precision down to 2^-28 of it.
 template <int J, int C>
-__device__ void own_chunk(const SharedParams& p, const uint8_t* pool_h, int b, int t0, int t1, float unscale,
-                          unsigned char* scratch, float* rec, int lane) {
+__device__ void own_chunk(const SharedParams& p, const uint8_t* pool_h, int b, int t0, int t1, float scale,
+                          float unscale, unsigned char* scratch, float* rec, int lane) {
   using T = Shape<J, C>;
   constexpr int LB = T::LB, NW = T::NW;
   const int side = lane / J, j = lane % J;
   const bool act = side < T::TPS;
   const uint32_t sa = u32s(scratch);
-  float* pw = reinterpret_cast<float*>(scratch + kOwnP);
-  OwnState<C> s;
-  s.m = -INFINITY;
-  s.l = 0.f;
+  float m = -INFINITY, l = 0.f, o[C];
 #pragma unroll
-  for (int c = 0; c < C; ++c) s.o[c] = 0.f;
+  for (int c = 0; c < C; ++c) o[c] = 0.f;
   const int32_t* bt = p.block_table + static_cast<int64_t>(b) * p.max_pages_per_seq;
   const int b0 = t0 / LB, b1 = (t1 + LB - 1) / LB;
   uint32_t kw[NW], vw[NW];
   auto entry_of = [&](int blk) { return blk < b1 ? __ldg(bt + (blk >> p.lbpp)) : -1; };
   bool ok = false;
-  auto request = [&](int blk, int entry) {                 // index rows of a block; false: nothing to read
+  auto request = [&](int blk, int entry) {                 // index rows of a block
     ok = blk < b1 && entry >= 0 && entry < p.n_pages;
     if (blk < b1 && !ok && lane == 0 && p.status != nullptr) atomicOr(p.status, LOOPVQ_DECODE_STATUS_BAD_PAGE);
 #pragma unroll
@@ -983,13 +982,6 @@ __device__ void own_chunk(const SharedParams& p, const uint8_t* pool_h, int b, i
       }
     }
   };
-  uint32_t at[NW];                                         // entry bytes of this slot's groups, packed
-#pragma unroll
-  for (int w = 0; w < NW; ++w) {
-    at[w] = 0u;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) at[w] |= static_cast<uint32_t>((4 * w + i + lane) % J * T::ENTRY) << (8 * i);
-  }
   int e_next = entry_of(b0);
   request(b0, e_next);
   e_next = entry_of(b0 + 1);
@@ -1019,57 +1011,78 @@ __device__ void own_chunk(const SharedParams& p, const uint8_t* pool_h, int b, i
     const int tok = blk * LB + lane;
     const bool valid = ok && lane < LB && tok >= t0 && tok < t1;
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    const uint32_t qa = sa + kOwnQ + lane * T::ENTRY;
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-      Word<T::ENTRY> e[4];
+      Word<T::ENTRY> e[4], qv[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)                          // (entry byte, codeword row)
-        e[i] = lds<T::ENTRY, kShBase + kKtabOff>(__byte_perm(kw[w], at[w], (4u + i) | (static_cast<uint32_t>(i) << 4)) & 0xffffu);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t qa = sa + kOwnQ + (lane + 4 * w + i) * (C * 4);
-#pragma unroll
-        for (int c = 0; c < C; c += 4) {
-          const Word<16> qv = lds<16, 0>(qa + c * 4);
-          const float2 k0 = half2_floats(e[i].w[c / 2]), k1 = half2_floats(e[i].w[c / 2 + 1]);
-          acc[i] = fmaf(__uint_as_float(qv.w[0]), k0.x, fmaf(__uint_as_float(qv.w[1]), k0.y, acc[i]));
-          acc[i] = fmaf(__uint_as_float(qv.w[2]), k1.x, fmaf(__uint_as_float(qv.w[3]), k1.y, acc[i]));
-        }
+      for (int i = 0; i < 4; ++i) {                        // codeword row (byte 1) | entry (byte 0)
+        const uint32_t at = J == 32 ? static_cast<uint32_t>(lane + 4 * w + i) * T::ENTRY      // byte 0 wraps by itself
+                                    : static_cast<uint32_t>((lane + 4 * w + i) % J) * T::ENTRY;
+        e[i] = lds<T::ENTRY, kShBase + kKtabOff>(__byte_perm(kw[w], at, 0x7704u | (static_cast<uint32_t>(i) << 4)));
+        qv[i] = lds<T::ENTRY, 0>(qa + (4 * w + i) * T::ENTRY);
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < C / 2; ++c) dot_f16(acc[i], qv[i].w[c], e[i].w[c]);
     }
     request(blk + 1, e_next);                              // lands under this block's values
     e_next = entry_of(blk + 2);
-    const float x = valid ? (acc[0] + acc[1]) + (acc[2] + acc[3]) : -INFINITY;
-    own_raise<C>(s, redux_fmax(x));
-    const float w0 = fast_exp2(x - (s.m == -INFINITY ? 0.f : s.m));
-    s.l += w0;
-    pw[lane] = w0;
+    const float x = valid ? ((acc[0] + acc[1]) + (acc[2] + acc[3])) * scale : -INFINITY;
+    const float mx = redux_fmax(x) - 14.f;
+    if (mx > m) {                                          // warp-uniform
+      const float f = m == -INFINITY ? 0.f : fast_exp2(m - mx);
+      l *= f;
+#pragma unroll
+      for (int c = 0; c < C; ++c) o[c] *= f;
+      m = mx;
+    }
+    const float w0 = fast_exp2(x - (m == -INFINITY ? 0.f : m));
+    l += w0;
+    const __half wh = __float2half_rn(w0);
+    asm volatile("st.shared.b16 [%0], %1;" ::"r"(sa + kOwnP + lane * 2), "h"(*reinterpret_cast<const uint16_t*>(&wh)) : "memory");
     __syncwarp();
     if (act) {
       const uint32_t row = sa + kOwnRows + side * J * kOwnPitch + j;
-      const uint32_t wa = sa + kOwnP + side * J * 4;
+      const uint32_t wa = sa + kOwnP + side * J * 2;
 #pragma unroll
       for (int k = 0; k < J; k += 4) {
-        const Word<16> w4 = lds<16, 0>(wa + k * 4);
+        const Word<8> w4 = lds<8, 0>(wa + k * 2);
         uint32_t iv[4];
+        Word<T::ENTRY> e[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           asm volatile("ld.shared.u8 %0, [%1];" : "=r"(iv[i]) : "r"(row + (k + i) * kOwnPitch + J - (k + i)));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const Word<T::ENTRY> e = lds<T::ENTRY, kShBase + kVtabOff>(iv[i] * 256u + j * T::ENTRY);
-          const float w = __uint_as_float(w4.w[i]);
+        for (int i = 0; i < 4; ++i) e[i] = lds<T::ENTRY, kShBase + kVtabOff>(iv[i] * 256u + j * T::ENTRY);
 #pragma unroll
-          for (int c = 0; c < C; c += 2) {
-            const float2 f = half2_floats(e.w[c / 2]);
-            s.o[c] = fmaf(w, f.x, s.o[c]);
-            s.o[c + 1] = fmaf(w, f.y, s.o[c + 1]);
-          }
+        for (int c = 0; c < C / 2; ++c) {
+          axpy_f16<0>(o[2 * c], o[2 * c + 1], w4.w[0], e[0].w[c]);
+          axpy_f16<1>(o[2 * c], o[2 * c + 1], w4.w[0], e[1].w[c]);
+          axpy_f16<0>(o[2 * c], o[2 * c + 1], w4.w[1], e[2].w[c]);
+          axpy_f16<1>(o[2 * c], o[2 * c + 1], w4.w[1], e[3].w[c]);
         }
       }
     }
   }
-  own_record<J, C>(s, unscale, rec, lane);
+  l = warp_sum(l);
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    float t = o[c];
+#pragma unroll
+    for (int k = 1; k < T::TPS; ++k) t += __shfl_sync(0xffffffffu, o[c], (lane + k * J) & 31);
+    o[c] = t * unscale;
+  }
+  if (lane < J) {
+#pragma unroll
+    for (int c = 0; c < C; c += 4)
+      *reinterpret_cast<float4*>(rec + 4 + lane * C + c) = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+  }
+  if (lane == 0) {
+    rec[0] = l == l ? m : NAN;
+    rec[1] = l;
+  }
 }
 
 // Runs beside the shared grid, on the SMs that it leaves free: the shared blocks
@@ -1101,9 +1114,12 @@ __global__ void __launch_bounds__(kOwnWarps * 32, 1) shared_own_kernel(const Sha
                                  : (LOOPVQ_DECODE_STATUS_TIMEOUT | LOOPVQ_DECODE_STATUS_UNDRAINED));
   }
   const int* exk = p.exps + hkv * 64;
+  float* fk = reinterpret_cast<float*>(sm + kOwnFkOff);
+  if (tid < J) fk[tid] = ldexpf(1.f, -__ldg(exk + tid));
+  __syncthreads();
   const float unv = lane < J ? ldexpf(1.f, -__ldg(exk + 32 + lane)) : 0.f;   // of this lane's record channels
-  unsigned char* scratch = sm + kKtileOff + warp * kOwnBytes;
-  float* qs = reinterpret_cast<float*>(scratch + kOwnQ);
+  unsigned char* scratch = sm + kOwnScratch + warp * kOwnBytes;
+  uint32_t* qs = reinterpret_cast<uint32_t*>(scratch + kOwnQ);
   const uint8_t* pool_h = p.pool_lg + hkv * p.pool_stride_head;
   const int64_t tasks = static_cast<int64_t>(p.B) * p.ratio * p.NC;
   for (int64_t t = static_cast<int64_t>(part) * kOwnWarps + warp; t < tasks;
@@ -1112,10 +1128,6 @@ __global__ void __launch_bounds__(kOwnWarps * 32, 1) shared_own_kernel(const Sha
     const int64_t y = t / p.NC;
     const int r = static_cast<int>(y % p.ratio), b = static_cast<int>(y / p.ratio);
     const int64_t pair = static_cast<int64_t>(b) * p.Hq + hkv * p.ratio + r;
-    const int n_vq = seq_vq(p, b);
-    const int g = group_of(p, b, lane);
-    const int s0 = g < 0 ? 0 : min(group_shared(p, g), n_vq);
-    const int n_own = min(n_vq - s0, p.max_own);
     float* rec = p.orec + (pair * p.NC + ck + 1) * T::RS;
     if (failed) {
       if (lane == 0) {
@@ -1125,23 +1137,36 @@ __global__ void __launch_bounds__(kOwnWarps * 32, 1) shared_own_kernel(const Sha
       continue;
     }
     if (ck < 0) {
-      if (hkv == 0 && r == 0 && lane == 0 && n_own < n_vq - s0 && p.status != nullptr)
-        atomicOr(p.status, LOOPVQ_DECODE_STATUS_BAD_GROUP);
-      float q[C];
-#pragma unroll
-      for (int c = 0; c < C; ++c)
-        q[c] = lane / J < T::TPS ? bf16_bits_to_float(p.q[pair * D + lane % J * C + c]) * p.scale_log2 : 0.f;
-      own_window<J, C>(p, static_cast<int64_t>(b) * p.Hkv + hkv, max(0, min(__ldg(p.seq_lens + b), p.W)), q, rec, lane);
+      own_window<D>(p, static_cast<int64_t>(b) * p.Hkv + hkv, max(0, min(__ldg(p.seq_lens + b), p.W)), p.q + pair * D, rec, lane);
       continue;
     }
-    const int t0 = s0 + ck * p.CH, t1 = min(s0 + n_own, t0 + p.CH);
+    const int2 seq = __ldg(p.seqs + b);                    // its shared tokens, its own
+    const int t0 = seq.x + ck * p.CH, t1 = min(seq.x + seq.y, t0 + p.CH);
     if (t0 >= t1) continue;                                // the merge does not read it
+    // the query in fp16 against the scales of the key groups: word i holds
+    // channels 2i, 2i + 1 (of D, then around again)
+    static_assert((31 + J) * C * 2 <= kOwnP - kOwnQ, "query entries 0 .. 30 + J fit");
+    const uint32_t* qw = reinterpret_cast<const uint32_t*>(p.q + pair * D);
+    constexpr int QW = (31 + J) * C / 2, PER = (QW + 31) / 32;
+    float2 f[PER];
+    float top = 0.f;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int i = (lane + 32 * k) % (D / 2);
+      f[k] = bf16x2_to_float2(__ldg(qw + i));
+      const float g = fk[2 * i / C];
+      f[k].x *= g;
+      f[k].y *= g;
+      top = fmaxf(top, fmaxf(finite_abs(f[k].x), finite_abs(f[k].y)));
+    }
+    const int kq = scale_exp(redux_fmax(top));
+    const float fq = ldexpf(1.f, kq);
     __syncwarp();
-    static_assert((31 + J) * C * 4 <= kOwnP - kOwnQ, "query entries 0 .. 30 + J fit");
-    for (int i = lane; i < (31 + J) * C; i += 32) 
-      qs[i] = ldexpf(bf16_bits_to_float(p.q[pair * D + i % D]) * p.scale_log2, -__ldg(exk + i % D / C));
+#pragma unroll
+    for (int k = 0; k < PER; ++k)
+      if (lane + 32 * k < QW) qs[lane + 32 * k] = half2_bits(f[k].x * fq, f[k].y * fq);
     __syncwarp();
-    own_chunk<J, C>(p, pool_h, b, t0, t1, unv, scratch, rec, lane);
+    own_chunk<J, C>(p, pool_h, b, t0, t1, ldexpf(p.scale_log2, -kq), unv, scratch, rec, lane);
   }
   // the merge waits for this grid, which ends after the shared one
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1166,11 +1191,8 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(const SharedParams p)
   const int64_t pair = static_cast<int64_t>(blockIdx.x) * 4 + warp;
   if (pair >= static_cast<int64_t>(p.B) * p.Hq) return;
   const int b = static_cast<int>(pair / p.Hq);
-  const int n_vq = seq_vq(p, b);
-  const int g = group_of(p, b, lane);
-  const int s0 = g < 0 ? 0 : min(group_shared(p, g), n_vq);
-  const int n_own = min(n_vq - s0, p.max_own);
-  const int ns = g < 0 ? 0 : p.NS, nc = 1 + (n_own + p.CH - 1) / p.CH;   // the window's record first
+  const int2 seq = __ldcg(p.seqs + b);
+  const int ns = seq.x > 0 ? p.NS : 0, nc = 1 + (seq.y + p.CH - 1) / p.CH;   // the window's record first
   float m = -INFINITY, l = 0.f, o[NCH];
 #pragma unroll
   for (int c = 0; c < NCH; ++c) o[c] = 0.f;
@@ -1316,7 +1338,7 @@ loopvq_status launch_shared_jc(const SharedParams& p, int N, cudaStream_t st) {
   if (s != LOOPVQ_OK) return s;
   shared_table_kernel<J, C><<<dim3(J / 4, 2, p.Hkv), kE, 0, st>>>(p.cb_k, p.cb_v, p.cb_stride_head,
                                                                   const_cast<unsigned char*>(p.tables),
-                                                                  const_cast<int*>(p.exps));
+                                                                  const_cast<int*>(p.exps), p);
   if (cudaGetLastError() != cudaSuccess) return LOOPVQ_ERR_CUDA;
   if (p.shared_blocks > 0) {
     s = N == 16 ? launch_prefix<J, C, 16>(p, st) : N == 32 ? launch_prefix<J, C, 32>(p, st) : launch_prefix<J, C, 64>(p, st);
@@ -1346,7 +1368,7 @@ size_t shared_attn_workspace_bytes(const Geometry& g, int batch, int n_groups, i
                                    int max_own) {
   const SharedPlan q = make_plan(g, batch, n_groups, max_group, max_shared, max_own);
   return kStatusBytes + record_bytes(g, batch, q.NS) + record_bytes(g, batch, q.NC) +
-         static_cast<size_t>(g.Hkv) * (2 * kTabBytes + 64 * sizeof(int));
+         static_cast<size_t>(g.Hkv) * (2 * kTabBytes + 64 * sizeof(int)) + static_cast<size_t>(batch) * sizeof(int2);
 }
 
 loopvq_status launch_shared_attn(const SharedArgs& a) {
@@ -1376,6 +1398,7 @@ loopvq_status launch_shared_attn(const SharedArgs& a) {
   char* tables = reinterpret_cast<char*>(p.orec) + record_bytes(g, a.batch, q.NC);
   p.tables = reinterpret_cast<unsigned char*>(tables);
   p.exps = reinterpret_cast<int*>(tables + static_cast<size_t>(g.Hkv) * 2 * kTabBytes);
+  p.seqs = reinterpret_cast<int2*>(const_cast<int*>(p.exps) + static_cast<size_t>(g.Hkv) * 64);
   p.out = a.out;
   p.lse = a.lse;
   p.B = a.batch;
