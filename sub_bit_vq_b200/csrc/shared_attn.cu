@@ -64,7 +64,7 @@ constexpr int kShWarps = kMmaWarp + 1;
 constexpr int kShThreads = kShWarps * 32;
 // Registers of a thread: 72 at launch. With 64 query rows the softmax warps need
 // more and take what the filling warps give (8 x 104 + 16 x 56 = 24 x 72).
-constexpr int kSoftRegs = 104, kDeqRegs = 56;
+constexpr int kLaunchRegs = 72, kSoftRegs = 104, kDeqRegs = 56;
 constexpr int kTileRows = 128;            // token rows of a tile (4 index blocks of up to 32 slots)
 constexpr int kMaxRows = 64;              // query rows of a block
 constexpr float kRaise = 14.f;            // log2: a weight reaches 2^14 at most
@@ -122,15 +122,16 @@ struct SharedParams {
   const unsigned char* tables;    // [Hkv][K, V] fp16 tables of kTabBytes
   const int* exps;                // [Hkv][K, V][32]: a group's table entries are scaled by 2^exps
   int2* seqs;                     // [B] shared and own quantised tokens of a sequence
-  float* srec;                    // [pairs][NS][4 + d] records of the shared blocks
+  float* srec;                    // [pairs + shared_blocks * N][4 + d] records of the shared blocks
   float* orec;                    // [pairs][NC][4 + d] records of the own chunks
   int* status;
   void* out;
   float* lse;
   int B, n_groups, Hq, Hkv, ratio, W, Pg, n_pages, max_pages_per_seq;
   int max_group, max_shared, max_own;
-  int NS, RT, NC, CH;             // splits, row tiles, own records (window, chunks), tokens of a chunk
-  int shared_blocks, own_parts;   // grids: shared blocks; Hkv * own_parts own blocks
+  int2* spans;                    // [pairs] first shared record of a row, and their number (N records apart)
+  int NC, CH;                     // own records of a pair (window, chunks), tokens of a chunk
+  int shared_blocks, own_blocks;  // grids
   int lbpp;                       // log2 of the index blocks of a page
   float scale_log2;
 };
@@ -370,9 +371,6 @@ __device__ __forceinline__ void request_tables(const SharedParams& p, unsigned c
                  "l"(src + part * (kTabBytes / 2)), "r"(kTabBytes / 2), "r"(bar) : "memory");
 }
 
-// Number of shared tiles of split s of T tiles over NS splits: [first, last).
-__device__ __forceinline__ int split_tile(int T, int s, int NS) { return static_cast<int>(static_cast<int64_t>(T) * s / NS); }
-
 // Dequantises this lane's slot of a block: the w_n (up to W0) index words iw of
 // its row select entries of the table TAB, stored to its row of the tile TILE
 // at the places `at` gives (zeros for a slot at or past nv).
@@ -404,8 +402,25 @@ __device__ __forceinline__ void fill_block(const uint32_t (&iw)[W0], const uint3
 
 // ---- shared blocks ---------------------------------------------------------------
 
+// One run of tiles of a unit (group, row tile, head) in a block.
+struct Segment {
+  int g, rt, hkv, lo, rows;       // lo: the group's first sequence; rows: the unit's query rows
+  int S, tile0, nt;               // shared tokens of the group, tiles [tile0, tile0 + nt)
+  int64_t rec;                    // record of row 0
+  bool load;                      // the head's tables are not in shared memory yet
+};
+
+// Query row c of the unit as (sequence, query head).
+template <int N>
+__device__ __forceinline__ int64_t pair_of(const SharedParams& p, const Segment& u, int c) {
+  const int r = u.rt * N + c;
+  return static_cast<int64_t>(u.lo + r / p.ratio) * p.Hq + u.hkv * p.ratio + r % p.ratio;
+}
+
+// Returns false when a bounded wait gave up (the status word is flagged, the
+// records are NaN and nothing is in flight, or the flag says so).
 template <int J, int C, int N>
-__device__ void shared_block(const SharedParams& p, unsigned char* sm, int unit) {
+__device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const Segment& u, uint32_t tmem) {
   using T = Shape<J, C>;
   constexpr int D = T::D, NC = N / 2;
   // P: rows of 64 query rows and one buffer, or of 32 and two (the same bytes)
@@ -416,55 +431,18 @@ __device__ void shared_block(const SharedParams& p, unsigned char* sm, int unit)
   int* lim = reinterpret_cast<int*>(sm + kLimOff);
   volatile int* nvs = reinterpret_cast<volatile int*>(sm + kNvOff);
   float* red = reinterpret_cast<float*>(sm + kRedOff);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kTmemSlotOff);
   auto bar = [&](int i) { return u32s(sm + kBarOff) + 8u * i; };
+  const int rows = u.rows, S = u.S, tile0 = u.tile0, nt = u.nt, lo = u.lo, hkv = u.hkv;
 
-  // unit = ((group * RT + row tile) * Hkv + head) * NS + split
-  const int split = unit % p.NS;
-  int x = unit / p.NS;
-  const int hkv = x % p.Hkv;
-  x /= p.Hkv;
-  const int rt = x % p.RT, g = x / p.RT;
-  const int lo = max(0, __ldg(p.group_starts + g)), hi = min(p.B, __ldg(p.group_starts + g + 1));
-  const int rows = min(max(0, min(hi - lo, p.max_group) * p.ratio - rt * N), N);   // this tile's query rows
-  const int S = group_shared(p, g);
-  const int tiles = (S + T::TOK - 1) / T::TOK;
-  const int tile0 = split_tile(tiles, split, p.NS), nt = split_tile(tiles, split + 1, p.NS) - tile0;
-  auto pair_of = [&](int c) {                              // (sequence, query head) of row c
-    const int r = rt * N + c;
-    return static_cast<int64_t>(lo + r / p.ratio) * p.Hq + hkv * p.ratio + r % p.ratio;
-  };
-  if (rows <= 0 || nt <= 0) {                              // block-uniform
-    asm volatile("griddepcontrol.wait;" ::: "memory");     // (the own grid relies on it)
-  }
-  if (rows <= 0) return;
-  if (nt <= 0) {
-    for (int c = tid; c < rows; c += kShThreads) {
-      float* rec = p.srec + (pair_of(c) * p.NS + split) * T::RS;
-      rec[0] = -INFINITY;
-      rec[1] = 0.f;
-    }
-    return;
-  }
-
-  // ---- setup: barriers, TMEM, tables, queries -----------------------------------
-  if (tid == 0) {
+  // ---- setup: barriers, tables, queries -------------------------------------------
+  if (tid == 0) {                                          // (kernel start, or after a segment's last barrier)
     for (int i = 0; i < kBars; ++i) {
-      const uint32_t n = (i == kBarK || i == kBarV) ? kDeqWarps
-                         : (i == kBarP0 || i == kBarP1) ? kSoftWarps
-                         : 1;
+      const uint32_t n = (i == kBarK || i == kBarV) ? kDeqWarps : (i == kBarP0 || i == kBarP1) ? kSoftWarps : 1;
       asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar(i)), "r"(n) : "memory");
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    if (u.load) request_tables(p, sm, hkv, bar(kBarTab));
   }
-  if (warp == kMmaWarp) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(u32s(tmem_slot)),
-                 "r"(kTmCols) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
-  asm volatile("griddepcontrol.wait;" ::: "memory");       // the tables are written
-  asm volatile("griddepcontrol.launch_dependents;");       // ... so the own grid may start
-  if (tid == 0) request_tables(p, sm, hkv, bar(kBarTab));
   const int* exk = p.exps + hkv * 64;
   // the queries, scaled into fp16 (against the scales of the key groups): piece =
   // 8 channels of a row
@@ -477,7 +455,7 @@ __device__ void shared_block(const SharedParams& p, unsigned char* sm, int unit)
     for (int k = 0; k < PER; ++k) {
       const int f = tid + k * kShThreads, c = f / (D / 8), part = f % (D / 8);
       uint4 t = make_uint4(0u, 0u, 0u, 0u);
-      if (f < PIECES && c < rows) t = *(reinterpret_cast<const uint4*>(p.q + pair_of(c) * D) + part);
+      if (f < PIECES && c < rows) t = *(reinterpret_cast<const uint4*>(p.q + pair_of<N>(p, u, c) * D) + part);
       const uint32_t w[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -502,7 +480,7 @@ __device__ void shared_block(const SharedParams& p, unsigned char* sm, int unit)
   const float scale = ldexpf(p.scale_log2, -kq);
   // a row's shared tokens, its unset reference, zero value rows past a block's slots
   for (int c = tid; c < N; c += kShThreads) {
-    lim[c] = c < rows ? min(S, seq_vq(p, static_cast<int>(pair_of(c) / p.Hq))) : INT_MAX;
+    lim[c] = c < rows ? min(S, seq_vq(p, static_cast<int>(pair_of<N>(p, u, c) / p.Hq))) : INT_MAX;
     m_ref[c] = m_ref[kMaxRows + c] = kUnset;
   }
   if constexpr (T::LB < 32) {
@@ -513,7 +491,6 @@ __device__ void shared_block(const SharedParams& p, unsigned char* sm, int unit)
   tc_before();
   __syncthreads();
   tc_after();
-  const uint32_t tmem = *tmem_slot;
   int min_lim = INT_MAX;
 #pragma unroll 1
   for (int c = 0; c < N; ++c) min_lim = min(min_lim, lim[c]);
@@ -579,7 +556,7 @@ __device__ void shared_block(const SharedParams& p, unsigned char* sm, int unit)
     };
     uint32_t w0[W0], w1[W0];                               // tiles i and i + 1
     int nv0 = load_rows(0, w0), nv1 = load_rows(1, w1);
-    failed = !mbar_wait(bar(kBarTab), 0, kShSpin);
+    if (u.load) failed = !mbar_wait(bar(kBarTab), 0, kShSpin);
 #pragma unroll 1
     for (int i = 0; i < nt; ++i) {
       // the tile is free when S^T (K) or O^T (V) of the tile before is done
@@ -603,6 +580,7 @@ __device__ void shared_block(const SharedParams& p, unsigned char* sm, int unit)
       nv0 = nv1;
       nv1 = load_rows(i + 2, w1);                          // lands during the next tile
     }
+    if constexpr (N > 32) reg_inc<kLaunchRegs>();
   } else if (warp == kMmaWarp) {
     // ---- the products --------------------------------------------------------------
     if (lane == 0) {
@@ -778,32 +756,161 @@ __device__ void shared_block(const SharedParams& p, unsigned char* sm, int unit)
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           if (c0 + c + k < rows && row < D)
-            p.srec[(pair_of(c0 + c + k) * p.NS + split) * T::RS + 4 + row] = __uint_as_float(o[k]) * unscale;
+            p.srec[(u.rec + c0 + c + k) * T::RS + 4 + row] = __uint_as_float(o[k]) * unscale;
         }
       }
       named_sync(bar_id, 128);
       if (quad == 0 && lane < NC && c0 + lane < rows) {
         const int c = c0 + lane;
         const float t = cm[c] + cm[kMaxRows + c] + cm[2 * kMaxRows + c] + cm[3 * kMaxRows + c];
-        float* rec = p.srec + (pair_of(c) * p.NS + split) * T::RS;
+        float* rec = p.srec + (u.rec + c) * T::RS;
         rec[0] = t == 0.f ? -INFINITY : m_ref[mb * kMaxRows + c];
         rec[1] = t;
       }
     }
+    if constexpr (N > 32) reg_dec<kLaunchRegs>();
   }
   const bool any_failed = __syncthreads_or(failed);
   if (any_failed) {
     // a bounded wait gave up: wait for what was issued, flag, poison the records
     if (tid == kMmaWarp * 32) {
-      const bool drained = mbar_wait(bar(kBarDrain), 0, kShDrainSpin) && mbar_wait(bar(kBarTab), 0, kShDrainSpin);
+      const bool drained = mbar_wait(bar(kBarDrain), 0, kShDrainSpin) &&
+                           (!u.load || mbar_wait(bar(kBarTab), 0, kShDrainSpin));
       if (p.status != nullptr)
         atomicOr(p.status, drained ? LOOPVQ_DECODE_STATUS_TIMEOUT
                                    : (LOOPVQ_DECODE_STATUS_TIMEOUT | LOOPVQ_DECODE_STATUS_UNDRAINED));
     }
-    for (int c = tid; c < rows; c += kShThreads) {
-      float* rec = p.srec + (pair_of(c) * p.NS + split) * T::RS;
-      rec[0] = NAN;
-      rec[1] = 1.f;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    for (int i = 0; i < kBars; ++i) asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(bar(i)) : "memory");
+  }
+  return !any_failed;
+}
+
+// Tokens of the tensor-core setup of a unit, in tiles: what a block that starts
+// a unit spends on its tables, queries, first tile and records.
+constexpr int kSetupTiles = 5;
+
+// A persistent grid over the tiles of all units, heads outermost. A unit counts
+// kSetupTiles + its tiles; block c of n takes the c-th n-th of the total U, so
+// every block does the same work whatever the groups' sizes and lengths, and
+// meets one or a few units. Its records go to rows R + c*N .., R the rows of the
+// units before: since R and c both grow along the blocks, no two collide.
+template <int J, int C, int N>
+__global__ void __launch_bounds__(kShThreads, 1) shared_prefix_kernel(const SharedParams p) {
+  using T = Shape<J, C>;
+  extern __shared__ __align__(1024) unsigned char sm[];
+  if (u32s(sm) != kShBase) {                               // the host checks this before launching
+    if (threadIdx.x == 0 && p.status != nullptr) atomicOr(p.status, LOOPVQ_DECODE_STATUS_SHARED_BASE);
+    return;
+  }
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kTmemSlotOff);
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(u32s(tmem_slot)),
+                 "r"(kTmCols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  // group g: first sequence, query rows, shared tokens, cost of its row tiles per head
+  struct Group {
+    int lo, rows, S, tiles, cost;
+  };
+  auto group = [&](int g) {
+    Group r{0, 0, 0, 0, 0};
+    if (g < p.n_groups) {
+      r.lo = max(0, __ldg(p.group_starts + g));
+      r.rows = max(0, min(min(p.B, __ldg(p.group_starts + g + 1)) - r.lo, p.max_group)) * p.ratio;
+      r.S = group_shared(p, g);
+      r.tiles = (r.S + T::TOK - 1) / T::TOK;
+      r.cost = r.tiles > 0 ? (r.rows + N - 1) / N * (r.tiles + kSetupTiles) : 0;
+    }
+    return r;
+  };
+  // the cost of one head, and the group that cost `at` of it falls into (lane-uniform)
+  auto find = [&](int64_t at, int& g_out, int64_t& before) -> int64_t {
+    int64_t acc = 0;
+    g_out = -1;
+    before = 0;
+    for (int g0 = 0; g0 < p.n_groups; g0 += 32) {
+      const int cost = group(g0 + lane).cost;
+      int64_t incl = cost;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, cost > 0 && at >= acc + incl - cost && at < acc + incl);
+      if (hit != 0u) {
+        const int src = __ffs(hit) - 1;
+        g_out = g0 + src;
+        before = acc + __shfl_sync(0xffffffffu, incl - cost, src);
+      }
+      acc += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return acc;
+  };
+  int g = 0;
+  int64_t before;
+  const int64_t Ug = find(-1, g, before), U = Ug * p.Hkv;
+  const int64_t n = min(static_cast<int64_t>(gridDim.x), U);   // blocks with work
+  asm volatile("griddepcontrol.wait;" ::: "memory");       // the tables are written
+  asm volatile("griddepcontrol.launch_dependents;");       // ... so the own grid may start
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = *tmem_slot;
+  if (blockIdx.x < n) {                                    // block-uniform
+    int64_t at = U * blockIdx.x / n;
+    const int64_t end = U * (blockIdx.x + 1) / n;
+    int hkv = static_cast<int>(at / Ug), head_in_smem = -1;
+    find(at - hkv * Ug, g, before);
+    Group r = group(g);
+    int64_t off = at - hkv * Ug - before;
+    int rt = static_cast<int>(off / (r.tiles + kSetupTiles)), pos = static_cast<int>(off % (r.tiles + kSetupTiles));
+    bool ok = true;
+    while (at < end) {
+      const int cost = r.tiles + kSetupTiles;
+      const int take = static_cast<int>(min(static_cast<int64_t>(cost - pos), end - at));
+      Segment u;
+      u.g = g;
+      u.rt = rt;
+      u.hkv = hkv;
+      u.lo = r.lo;
+      u.rows = min(r.rows - rt * N, N);
+      u.S = r.S;
+      u.tile0 = max(pos - kSetupTiles, 0);
+      u.nt = max(pos + take - kSetupTiles, 0) - u.tile0;
+      const int64_t R = (static_cast<int64_t>(hkv) * p.B + r.lo) * p.ratio + rt * N;
+      u.rec = R + static_cast<int64_t>(blockIdx.x) * N;
+      u.load = hkv != head_in_smem;
+      if (pos == 0) {                                      // the unit's first block: where its rows' records are
+        const int64_t c0 = ((at + 1) * n - 1) / U, c1 = ((at + cost) * n - 1) / U;
+        for (int c = tid; c < u.rows; c += kShThreads)
+          p.spans[pair_of<N>(p, u, c)] = make_int2(static_cast<int>(R + c0 * N + c), static_cast<int>(c1 - c0 + 1));
+      }
+      if (u.nt > 0 && ok) {
+        ok = shared_segment<J, C, N>(p, sm, u, tmem);
+        head_in_smem = hkv;
+      }
+      if (u.nt <= 0 || !ok) {                              // no tiles, or given up
+        for (int c = tid; c < u.rows; c += kShThreads) {
+          p.srec[(u.rec + c) * T::RS] = ok ? -INFINITY : NAN;
+          p.srec[(u.rec + c) * T::RS + 1] = ok ? 0.f : 1.f;
+        }
+      }
+      at += take;
+      pos = 0;
+      if (++rt * N >= r.rows) {                            // next group with shared tokens, next head
+        rt = 0;
+        do {
+          if (++g == p.n_groups) {
+            g = 0;
+            ++hkv;
+          }
+          r = group(g);
+        } while (r.cost == 0 && at < end);
+      }
     }
   }
   tc_before();
@@ -1093,7 +1200,6 @@ __global__ void __launch_bounds__(kOwnWarps * 32, 1) shared_own_kernel(const Sha
   constexpr int D = T::D;
   extern __shared__ __align__(1024) unsigned char sm[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int hkv = blockIdx.x % p.Hkv, part = blockIdx.x / p.Hkv;
   const uint32_t bar = u32s(sm + kOwnBarOff);
   if (u32s(sm) != kShBase) {                               // the host checks this before launching
     if (tid == 0 && p.status != nullptr) atomicOr(p.status, LOOPVQ_DECODE_STATUS_SHARED_BASE);
@@ -1105,25 +1211,35 @@ __global__ void __launch_bounds__(kOwnWarps * 32, 1) shared_own_kernel(const Sha
   }
   __syncthreads();
   if (p.shared_blocks == 0) asm volatile("griddepcontrol.wait;" ::: "memory");   // this grid follows the tables' own
-  if (tid == 0) request_tables(p, sm, hkv, bar);
-  const bool failed = __syncthreads_or(!mbar_wait(bar, 0, kShSpin));
-  if (failed && tid == 0) {                                // no copy may outlive the block
-    const bool drained = mbar_wait(bar, 0, kShDrainSpin);
-    if (p.status != nullptr)
-      atomicOr(p.status, drained ? LOOPVQ_DECODE_STATUS_TIMEOUT
-                                 : (LOOPVQ_DECODE_STATUS_TIMEOUT | LOOPVQ_DECODE_STATUS_UNDRAINED));
-  }
-  const int* exk = p.exps + hkv * 64;
   float* fk = reinterpret_cast<float*>(sm + kOwnFkOff);
-  if (tid < J) fk[tid] = ldexpf(1.f, -__ldg(exk + tid));
-  __syncthreads();
-  const float unv = lane < J ? ldexpf(1.f, -__ldg(exk + 32 + lane)) : 0.f;   // of this lane's record channels
   unsigned char* scratch = sm + kOwnScratch + warp * kOwnBytes;
   uint32_t* qs = reinterpret_cast<uint32_t*>(scratch + kOwnQ);
-  const uint8_t* pool_h = p.pool_lg + hkv * p.pool_stride_head;
-  const int64_t tasks = static_cast<int64_t>(p.B) * p.ratio * p.NC;
-  for (int64_t t = static_cast<int64_t>(part) * kOwnWarps + warp; t < tasks;
-       t += static_cast<int64_t>(p.own_parts) * kOwnWarps) {
+  // tasks (head, sequence, query head of it, window or chunk), heads outermost; the
+  // block takes its share of the list, one or a few heads
+  const int64_t per_head = static_cast<int64_t>(p.B) * p.ratio * p.NC;
+  const int64_t t_lo = per_head * p.Hkv * blockIdx.x / gridDim.x, t_hi = per_head * p.Hkv * (blockIdx.x + 1) / gridDim.x;
+  bool failed = false;
+  int phase = 0;
+  for (int64_t th = t_lo; th < t_hi; ++phase) {            // block-uniform
+   const int hkv = static_cast<int>(th / per_head);
+   const int64_t t_end = min(t_hi, (hkv + 1) * per_head);
+   const int* exk = p.exps + hkv * 64;
+   if (!failed) {
+    __syncthreads();                                       // the head before is done with tables and scales
+    if (tid == 0) request_tables(p, sm, hkv, bar);
+    if (tid < J) fk[tid] = ldexpf(1.f, -__ldg(exk + tid));
+    failed = __syncthreads_or(!mbar_wait(bar, phase & 1, kShSpin));
+    if (failed && tid == 0) {                              // no copy may outlive the block
+      const bool drained = mbar_wait(bar, phase & 1, kShDrainSpin);
+      if (p.status != nullptr)
+        atomicOr(p.status, drained ? LOOPVQ_DECODE_STATUS_TIMEOUT
+                                   : (LOOPVQ_DECODE_STATUS_TIMEOUT | LOOPVQ_DECODE_STATUS_UNDRAINED));
+    }
+   }
+   const float unv = lane < J ? ldexpf(1.f, -__ldg(exk + 32 + lane)) : 0.f;   // of this lane's record channels
+   const uint8_t* pool_h = p.pool_lg + hkv * p.pool_stride_head;
+   for (int64_t ti = th + warp; ti < t_end; ti += kOwnWarps) {
+    const int64_t t = ti - hkv * per_head;
     const int ck = static_cast<int>(t % p.NC) - 1;         // -1: the window
     const int64_t y = t / p.NC;
     const int r = static_cast<int>(y % p.ratio), b = static_cast<int>(y / p.ratio);
@@ -1167,23 +1283,15 @@ __global__ void __launch_bounds__(kOwnWarps * 32, 1) shared_own_kernel(const Sha
       if (lane + 32 * k < QW) qs[lane + 32 * k] = half2_bits(f[k].x * fq, f[k].y * fq);
     __syncwarp();
     own_chunk<J, C>(p, pool_h, b, t0, t1, ldexpf(p.scale_log2, -kq), unv, scratch, rec, lane);
+   }
+   th = t_end;
   }
   // the merge waits for this grid, which ends after the shared one
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-template <int J, int C, int N>
-__global__ void __launch_bounds__(kShThreads, 1) shared_prefix_kernel(const SharedParams p) {
-  extern __shared__ __align__(1024) unsigned char sm[];
-  if (u32s(sm) != kShBase) {                               // the host checks this before launching
-    if (threadIdx.x == 0 && p.status != nullptr) atomicOr(p.status, LOOPVQ_DECODE_STATUS_SHARED_BASE);
-    return;
-  }
-  shared_block<J, C, N>(p, sm, blockIdx.x);
-}
-
 // One warp per (sequence, query head): joins the records that its blocks wrote.
-template <int D>
+template <int D, int N>
 __global__ void __launch_bounds__(128) shared_merge_kernel(const SharedParams p) {
   constexpr int RS = 4 + D, NCH = (D + 31) / 32;
   asm volatile("griddepcontrol.wait;" ::: "memory");       // every record is written
@@ -1192,7 +1300,8 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(const SharedParams p)
   if (pair >= static_cast<int64_t>(p.B) * p.Hq) return;
   const int b = static_cast<int>(pair / p.Hq);
   const int2 seq = __ldcg(p.seqs + b);
-  const int ns = seq.x > 0 ? p.NS : 0, nc = 1 + (seq.y + p.CH - 1) / p.CH;   // the window's record first
+  const int2 span = seq.x > 0 ? __ldcg(p.spans + pair) : make_int2(0, 0);
+  const int ns = span.y, nc = 1 + (seq.y + p.CH - 1) / p.CH;   // the window's record first
   float m = -INFINITY, l = 0.f, o[NCH];
 #pragma unroll
   for (int c = 0; c < NCH; ++c) o[c] = 0.f;
@@ -1203,7 +1312,7 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(const SharedParams p)
       const int r = r0 + k;
       mr[k] = -INFINITY;
       lr[k] = 0.f;
-      const float* rec = r < ns ? p.srec + (pair * p.NS + r) * RS : p.orec + (pair * p.NC + r - ns) * RS;
+      const float* rec = r < ns ? p.srec + (span.x + static_cast<int64_t>(r) * N) * RS : p.orec + (pair * p.NC + r - ns) * RS;
       const bool ok = r < ns + nc;
       if (ok) {
         mr[k] = __ldcg(rec);
@@ -1238,8 +1347,7 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(const SharedParams p)
 // How a call is cut up; a function of the sizes alone, so that the workspace
 // can be sized without a device.
 struct SharedPlan {
-  int N, RT, NS, NC, CH, own_parts;
-  int64_t shared_blocks;
+  int N, NC, CH, shared_blocks, own_blocks;
 };
 constexpr int kPlanSms = 148;             // blocks that run at once (one per SM of a B200)
 
@@ -1248,41 +1356,27 @@ SharedPlan make_plan(const Geometry& g, int batch, int n_groups, int max_group, 
   const int ratio = g.Hq / g.Hkv;
   const int64_t rows = static_cast<int64_t>(max_group) * ratio;
   q.N = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-  q.RT = static_cast<int>((rows + q.N - 1) / q.N);
-  q.CH = 128;
+  q.CH = 256;
   while ((max_own + q.CH - 1) / q.CH > 64) q.CH *= 2;
   q.NC = 1 + (max_own + q.CH - 1) / q.CH;                  // the window, and the chunks
+  // Both grids together fill the machine once, shared by their work (SM cycles,
+  // measured: a tile, a unit's setup, an own or window token).
+  const double t_tile = q.N > 32 ? 3300 : 2100, t_token = 13;
   const int tiles = (max_shared + 4 * g.LB - 1) / (4 * g.LB);
-  const int64_t units = max_shared > 0 ? static_cast<int64_t>(n_groups) * q.RT * g.Hkv : 0;
-  const int64_t tasks = static_cast<int64_t>(batch) * ratio * q.NC;      // warps' tasks of one head
-  // rough block times (cycles): setup, a tile, a task of a whole chunk
-  const double setup = 6000, t_tile = 1800, t_task = 6000;
-  const double work_a = units * (tiles * t_tile), work_b = g.Hkv * (tasks * t_task / kOwnWarps);
-  int parts = static_cast<int>(kPlanSms / g.Hkv * work_b / (work_a + work_b + 1) + 0.5);
-  if (parts < 1) parts = 1;
-  const int64_t most = (tasks + kOwnWarps - 1) / kOwnWarps;
-  int64_t room = kPlanSms - static_cast<int64_t>(parts) * g.Hkv;
-  q.NS = 1;
+  const double units = max_shared > 0 ? (static_cast<double>(batch) * ratio / q.N + n_groups) * g.Hkv : 0;
+  const double work_a = units * (tiles + 5) * t_tile;
+  const double work_b = static_cast<double>(batch) * g.Hq * (max_own * 0.75 + g.W) * t_token;
+  const int64_t tasks = static_cast<int64_t>(batch) * g.Hq * q.NC;
+  const int64_t most_b = (tasks + 15) / 16;
+  int64_t nb = static_cast<int64_t>(kPlanSms * work_b / (work_a + work_b) + 0.5);
+  nb = nb < 1 ? 1 : nb;
+  if (units > 0 && nb > kPlanSms - 1) nb = kPlanSms - 1;
+  q.own_blocks = static_cast<int>(nb < most_b ? nb : most_b);
   if (units > 0) {
-    if (room >= units) {
-      q.NS = static_cast<int>(room / units);
-    } else {                                               // several waves: the split with the least idle tail
-      double best = 0;
-      for (int ns = 1; ns <= 8; ++ns) {
-        const double waves = static_cast<double>((units * ns + kPlanSms - 1) / kPlanSms);
-        const double t = waves * (setup + (tiles + ns - 1) / ns * t_tile);
-        if (ns == 1 || t < best) {
-          best = t;
-          q.NS = ns;
-        }
-      }
-      parts = static_cast<int>(work_b / g.Hkv / (setup + (tiles + q.NS - 1) / q.NS * t_tile) + 1);
-    }
-    if (q.NS > tiles) q.NS = tiles;
-    if (q.NS > 64) q.NS = 64;
+    const double most_a = units * tiles;
+    const int na = kPlanSms - static_cast<int>(nb);
+    q.shared_blocks = most_a < na ? static_cast<int>(most_a) : na;
   }
-  q.own_parts = static_cast<int>(parts < most ? parts : most);
-  q.shared_blocks = units * q.NS;
   return q;
 }
 
@@ -1344,14 +1438,31 @@ loopvq_status launch_shared_jc(const SharedParams& p, int N, cudaStream_t st) {
     s = N == 16 ? launch_prefix<J, C, 16>(p, st) : N == 32 ? launch_prefix<J, C, 32>(p, st) : launch_prefix<J, C, 64>(p, st);
     if (s != LOOPVQ_OK) return s;
   }
-  s = launch_after(shared_own_kernel<J, C>, static_cast<int64_t>(p.Hkv) * p.own_parts, kOwnWarps * 32, kOwnSmem, st, p);
+  s = launch_after(shared_own_kernel<J, C>, p.own_blocks, kOwnWarps * 32, kOwnSmem, st, p);
   if (s != LOOPVQ_OK) return s;
   const int64_t pairs = static_cast<int64_t>(p.B) * p.Hq;
-  return launch_after(shared_merge_kernel<J * C>, (pairs + 3) / 4, 128, 0, st, p);
+  switch (N) {
+    case 16: return launch_after(shared_merge_kernel<J * C, 16>, (pairs + 3) / 4, 128, 0, st, p);
+    case 32: return launch_after(shared_merge_kernel<J * C, 32>, (pairs + 3) / 4, 128, 0, st, p);
+    default: return launch_after(shared_merge_kernel<J * C, 64>, (pairs + 3) / 4, 128, 0, st, p);
+  }
 }
 
-size_t record_bytes(const Geometry& g, int batch, int slots) {
-  return static_cast<size_t>(batch) * g.Hq * slots * (4 + g.d) * sizeof(float);
+// Byte offsets of the workspace's parts.
+struct SharedLayout {
+  size_t srec, orec, tables, exps, spans, seqs, end;
+};
+SharedLayout make_layout(const Geometry& g, int batch, const SharedPlan& q) {
+  const size_t rec = (4 + static_cast<size_t>(g.d)) * sizeof(float), pairs = static_cast<size_t>(batch) * g.Hq;
+  SharedLayout w;
+  w.srec = kStatusBytes;
+  w.orec = w.srec + (q.shared_blocks > 0 ? pairs + static_cast<size_t>(q.shared_blocks) * q.N : 0) * rec;
+  w.tables = w.orec + pairs * q.NC * rec;
+  w.exps = w.tables + static_cast<size_t>(g.Hkv) * 2 * kTabBytes;
+  w.spans = w.exps + static_cast<size_t>(g.Hkv) * 64 * sizeof(int);
+  w.seqs = w.spans + pairs * sizeof(int2);
+  w.end = w.seqs + static_cast<size_t>(batch) * sizeof(int2);
+  return w;
 }
 
 }  // namespace
@@ -1366,15 +1477,14 @@ bool shared_attn_supported(const Geometry& g, int n_groups, int out_dtype) {
 
 size_t shared_attn_workspace_bytes(const Geometry& g, int batch, int n_groups, int max_group, int max_shared,
                                    int max_own) {
-  const SharedPlan q = make_plan(g, batch, n_groups, max_group, max_shared, max_own);
-  return kStatusBytes + record_bytes(g, batch, q.NS) + record_bytes(g, batch, q.NC) +
-         static_cast<size_t>(g.Hkv) * (2 * kTabBytes + 64 * sizeof(int)) + static_cast<size_t>(batch) * sizeof(int2);
+  return make_layout(g, batch, make_plan(g, batch, n_groups, max_group, max_shared, max_own)).end;
 }
 
 loopvq_status launch_shared_attn(const SharedArgs& a) {
   const Geometry& g = *a.geo;
   const SharedPlan q = make_plan(g, a.batch, a.n_groups, a.max_group, a.max_shared, a.max_own);
-  if (q.shared_blocks + static_cast<int64_t>(g.Hkv) * q.own_parts > INT_MAX / 2) return LOOPVQ_ERR_UNSUPPORTED;
+  // (records are counted in 32 bits)
+  if (static_cast<int64_t>(a.batch) * g.Hq > INT_MAX / 2) return LOOPVQ_ERR_UNSUPPORTED;
   const int gamma = a.loop_step / g.g, tau = a.loop_step % g.g;
   SharedParams p{};
   p.q = static_cast<const uint16_t*>(a.q);
@@ -1393,12 +1503,13 @@ loopvq_status launch_shared_attn(const SharedArgs& a) {
   p.win_v = static_cast<const uint16_t*>(a.win_v);
   char* ws = static_cast<char*>(a.workspace);
   p.status = reinterpret_cast<int*>(ws);
-  p.srec = reinterpret_cast<float*>(ws + kStatusBytes);
-  p.orec = reinterpret_cast<float*>(ws + kStatusBytes + record_bytes(g, a.batch, q.NS));
-  char* tables = reinterpret_cast<char*>(p.orec) + record_bytes(g, a.batch, q.NC);
-  p.tables = reinterpret_cast<unsigned char*>(tables);
-  p.exps = reinterpret_cast<int*>(tables + static_cast<size_t>(g.Hkv) * 2 * kTabBytes);
-  p.seqs = reinterpret_cast<int2*>(const_cast<int*>(p.exps) + static_cast<size_t>(g.Hkv) * 64);
+  const SharedLayout w = make_layout(g, a.batch, q);
+  p.srec = reinterpret_cast<float*>(ws + w.srec);
+  p.orec = reinterpret_cast<float*>(ws + w.orec);
+  p.tables = reinterpret_cast<unsigned char*>(ws + w.tables);
+  p.exps = reinterpret_cast<int*>(ws + w.exps);
+  p.spans = reinterpret_cast<int2*>(ws + w.spans);
+  p.seqs = reinterpret_cast<int2*>(ws + w.seqs);
   p.out = a.out;
   p.lse = a.lse;
   p.B = a.batch;
@@ -1413,12 +1524,10 @@ loopvq_status launch_shared_attn(const SharedArgs& a) {
   p.max_group = a.max_group;
   p.max_shared = a.max_shared;
   p.max_own = a.max_own;
-  p.NS = q.NS;
-  p.RT = q.RT;
   p.NC = q.NC;
   p.CH = q.CH;
-  p.shared_blocks = static_cast<int>(q.shared_blocks);
-  p.own_parts = q.own_parts;
+  p.shared_blocks = q.shared_blocks;
+  p.own_blocks = q.own_blocks;
   while ((1 << p.lbpp) < g.Pg / g.LB) ++p.lbpp;
   p.scale_log2 = a.sm_scale * kLog2e;
   cudaStream_t st = static_cast<cudaStream_t>(a.stream);
