@@ -89,19 +89,21 @@ constexpr int kVtileOff = kKtileOff + kTileBytes;
 constexpr int kPOff = kVtileOff + kTileBytes;              // [128 tokens] rows of 128 B, or twice of 64 B
 constexpr int kQOff = kPOff + kTileRows * 128;             // [2 channel blocks][N][128 B]
 constexpr int kQBytes = kMaxRows * 256;
-constexpr int kMOff = kQOff + kQBytes;                     // float [2][64]: references
-constexpr int kCmOff = kMOff + 2 * kMaxRows * 4;           // float [4][64]: column maxima, then sums
-constexpr int kLimOff = kCmOff + 4 * kMaxRows * 4;         // int [64]: a row's shared tokens
+constexpr int kMOff = kQOff + kQBytes;                     // float [64]: references
+constexpr int kCmOff = kMOff + kMaxRows * 4;               // float [4][64]: column maxima, then sums
+constexpr int kAlOff = kCmOff + 4 * kMaxRows * 4;          // float [64]: factors of a raise
+constexpr int kLimOff = kAlOff + kMaxRows * 4;             // int [64]: a row's shared tokens
 constexpr int kNvOff = kLimOff + kMaxRows * 4;             // int [4 tiles][4 blocks]: valid slots
 constexpr int kRedOff = kNvOff + 64;                       // float [25]: block reduction
 constexpr int kBarOff = kRedOff + 112;                     // mbarriers
-constexpr int kTmemSlotOff = kBarOff + 96;
+constexpr int kSegOff = kBarOff + 96;                      // the block's segment and walk
+constexpr int kTmemSlotOff = kSegOff + 112;
 constexpr int kShSmem = kTmemSlotOff + 16;
 static_assert(kShSmem <= 227 * 1024, "shared memory above 227 KB");
 
 // K and V tile filled, S^T done (per buffer; its K tile is free), P written (per
 // buffer), O^T += done (by tile parity; its V tile and P are free).
-enum { kBarK = 0, kBarV, kBarS0, kBarS1, kBarP0, kBarP1, kBarO0, kBarO1, kBarTab, kBarDrain, kBars };
+enum { kBarK = 0, kBarV, kBarS0, kBarS1, kBarP0, kBarP1, kBarO0, kBarO1, kBarTabK, kBarTabV, kBarDrain, kBars };
 static_assert(kBars * 8 <= kTmemSlotOff - kBarOff, "barriers fit");
 
 constexpr uint32_t kTmCols = 256, kTmS = 0, kTmO = 128;    // TMEM columns: S^T twice 64, O^T 64
@@ -361,13 +363,13 @@ __global__ void __launch_bounds__(kE) shared_table_kernel(const float* cb_k, con
   for (int i = 0; i < C / 2; ++i) dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
 }
 
-// Requests both tables of a head into shared memory (one thread).
-__device__ __forceinline__ void request_tables(const SharedParams& p, unsigned char* sm, int hkv, uint32_t bar) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(2 * kTabBytes) : "memory");
-  const unsigned char* src = p.tables + static_cast<size_t>(hkv) * 2 * kTabBytes;
-  for (int part = 0; part < 4; ++part)
+// Requests a table of a head (which: 0 K, 1 V) into shared memory (one thread).
+__device__ __forceinline__ void request_table(const SharedParams& p, unsigned char* sm, int hkv, int which, uint32_t bar) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(kTabBytes) : "memory");
+  const unsigned char* src = p.tables + (static_cast<size_t>(hkv) * 2 + which) * kTabBytes;
+  for (int part = 0; part < 2; ++part)
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                     u32s(sm + kKtabOff + part * (kTabBytes / 2))),
+                     u32s(sm + which * kTabBytes + part * (kTabBytes / 2))),
                  "l"(src + part * (kTabBytes / 2)), "r"(kTabBytes / 2), "r"(bar) : "memory");
 }
 
@@ -402,12 +404,12 @@ __device__ __forceinline__ void fill_block(const uint32_t (&iw)[W0], const uint3
 
 // ---- shared blocks ---------------------------------------------------------------
 
-// One run of tiles of a unit (group, row tile, head) in a block.
+// One run of tiles of a unit (group, row tile, head) in a block, in shared memory.
 struct Segment {
-  int g, rt, hkv, lo, rows;       // lo: the group's first sequence; rows: the unit's query rows
+  int hkv, rt, lo, rows;          // lo: the group's first sequence; rows: the unit's query rows
   int S, tile0, nt;               // shared tokens of the group, tiles [tile0, tile0 + nt)
+  int load;                       // the head's tables are not in shared memory yet
   int64_t rec;                    // record of row 0
-  bool load;                      // the head's tables are not in shared memory yet
 };
 
 // Query row c of the unit as (sequence, query head).
@@ -428,11 +430,12 @@ __device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const S
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   float* m_ref = reinterpret_cast<float*>(sm + kMOff);
   float* cm = reinterpret_cast<float*>(sm + kCmOff);
+  float* al = reinterpret_cast<float*>(sm + kAlOff);
   int* lim = reinterpret_cast<int*>(sm + kLimOff);
   volatile int* nvs = reinterpret_cast<volatile int*>(sm + kNvOff);
   float* red = reinterpret_cast<float*>(sm + kRedOff);
   auto bar = [&](int i) { return u32s(sm + kBarOff) + 8u * i; };
-  const int rows = u.rows, S = u.S, tile0 = u.tile0, nt = u.nt, lo = u.lo, hkv = u.hkv;
+  const int rows = u.rows, S = u.S, tile0 = u.tile0, nt = u.nt, hkv = u.hkv;
 
   // ---- setup: barriers, tables, queries -------------------------------------------
   if (tid == 0) {                                          // (kernel start, or after a segment's last barrier)
@@ -441,9 +444,18 @@ __device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const S
       asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar(i)), "r"(n) : "memory");
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    if (u.load) request_tables(p, sm, hkv, bar(kBarTab));
+    if (u.load) {
+      request_table(p, sm, hkv, 0, bar(kBarTabK));
+      request_table(p, sm, hkv, 1, bar(kBarTabV));
+    }
   }
   const int* exk = p.exps + hkv * 64;
+  // a row's shared tokens and its unset reference (the last threads; the first ones
+  // have the queries)
+  if (const int c = kShThreads - 1 - tid; c < N) {
+    lim[c] = c < rows ? min(S, seq_vq(p, static_cast<int>(pair_of<N>(p, u, c) / p.Hq))) : INT_MAX;
+    m_ref[c] = kUnset;
+  }
   // the queries, scaled into fp16 (against the scales of the key groups): piece =
   // 8 channels of a row
   int kq;
@@ -478,11 +490,6 @@ __device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const S
     }
   }
   const float scale = ldexpf(p.scale_log2, -kq);
-  // a row's shared tokens, its unset reference, zero value rows past a block's slots
-  for (int c = tid; c < N; c += kShThreads) {
-    lim[c] = c < rows ? min(S, seq_vq(p, static_cast<int>(pair_of<N>(p, u, c) / p.Hq))) : INT_MAX;
-    m_ref[c] = m_ref[kMaxRows + c] = kUnset;
-  }
   if constexpr (T::LB < 32) {
     for (int i = tid; i < kTileBytes / 16; i += kShThreads)
       *reinterpret_cast<uint4*>(sm + kVtileOff + i * 16) = make_uint4(0u, 0u, 0u, 0u);
@@ -491,9 +498,7 @@ __device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const S
   tc_before();
   __syncthreads();
   tc_after();
-  int min_lim = INT_MAX;
-#pragma unroll 1
-  for (int c = 0; c < N; ++c) min_lim = min(min_lim, lim[c]);
+  const int min_lim = __reduce_min_sync(0xffffffffu, min(lim[lane % N], lim[(lane + 32) % N]));
   bool failed = false;                                     // this thread's wait gave up
   const int tok0 = tile0 * T::TOK;                         // first token of the split
 
@@ -516,7 +521,7 @@ __device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const S
     // this lane's row in block 0 of page 0 (granule of its first word)
     const uint8_t* rows0 = p.pool_lg + hkv * p.pool_stride_head + (values ? p.plane_bytes : 0) + lane * T::GR +
                            (J == 32 ? half * (T::LB * 16) : 0);
-    const int32_t* bt = p.block_table + static_cast<int64_t>(lo) * p.max_pages_per_seq;
+    const int32_t* bt = p.block_table + static_cast<int64_t>(u.lo) * p.max_pages_per_seq;
     const int blk0 = tile0 * 4 + blk;                      // this warp's block of tile i: blk0 + 4 i
     // page-table entries of this warp's blocks of tiles e0 .. e0 + 31 (lane = tile)
     int e0 = 0, entry;
@@ -556,7 +561,7 @@ __device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const S
     };
     uint32_t w0[W0], w1[W0];                               // tiles i and i + 1
     int nv0 = load_rows(0, w0), nv1 = load_rows(1, w1);
-    if (u.load) failed = !mbar_wait(bar(kBarTab), 0, kShSpin);
+    if (u.load) failed = !mbar_wait(bar(values ? kBarTabV : kBarTabK), 0, kShSpin);
 #pragma unroll 1
     for (int i = 0; i < nt; ++i) {
       // the tile is free when S^T (K) or O^T (V) of the tile before is done
@@ -632,7 +637,6 @@ __device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const S
     float l[NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) l[c] = 0.f;
-    int mb = 0;
     float4 m4[NC / 4];                                     // this half's references
 #pragma unroll
     for (int c = 0; c < NC / 4; ++c) m4[c] = make_float4(kUnset, kUnset, kUnset, kUnset);
@@ -644,7 +648,6 @@ __device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const S
       uint32_t sv[NC];
       tld<NC>(lanes + kTmS + (i & 1) * 64 + c0, sv);
       const int nv = nvs[(i & 3) * 4 + quad];
-      const float* m = m_ref + mb * kMaxRows + c0;
       tld_wait();
       if (nv < 32 && lane >= nv) {                         // no token in this slot
 #pragma unroll
@@ -673,24 +676,32 @@ __device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const S
         }
         __syncwarp();
         tc_after();
-        // raise the references that were passed; l and O^T shrink with them
+        // raise the references that were passed; l and O^T shrink with them. Lane c
+        // keeps column c's maximum over the warp's tokens.
+        float top = -INFINITY;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
           const float t = redux_fmax(__uint_as_float(sv[c]) * scale);
-          if (lane == 0) cm[quad * kMaxRows + c0 + c] = t;
+          if (lane == c) top = t;
         }
+        if (lane < NC) cm[quad * kMaxRows + c0 + lane] = top;
         named_sync(bar_id, 128);
-        float* mn = m_ref + (mb ^ 1) * kMaxRows + c0;
-        auto raised = [&](int c) {                         // the column's new reference
-          const float t = fmaxf(fmaxf(cm[c0 + c], cm[kMaxRows + c0 + c]),
-                                fmaxf(cm[2 * kMaxRows + c0 + c], cm[3 * kMaxRows + c0 + c]));
-          return t > m[c] + kRaise ? t - kTop : m[c];
-        };
+        if (quad == 0 && lane < NC) {
+          const int c = c0 + lane;
+          const float t = fmaxf(fmaxf(cm[c], cm[kMaxRows + c]), fmaxf(cm[2 * kMaxRows + c], cm[3 * kMaxRows + c]));
+          const float was = m_ref[c], now = t > was + kRaise ? t - kTop : was;
+          m_ref[c] = now;
+          al[c] = fast_exp2(was - now);
+        }
+        named_sync(bar_id, 128);                           // references and factors written; cm is free
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          const float r = raised(c);
-          l[c] *= fast_exp2(m[c] - r);
-          if (quad == 0 && lane == 0) mn[c] = r;
+        for (int c = 0; c < NC; c += 4) {
+          m4[c / 4] = *reinterpret_cast<const float4*>(m_ref + c0 + c);
+          const float4 f = *reinterpret_cast<const float4*>(al + c0 + c);
+          l[c] *= f.x;
+          l[c + 1] *= f.y;
+          l[c + 2] *= f.z;
+          l[c + 3] *= f.w;
         }
         if (i > 0) {
 #pragma unroll 1
@@ -699,16 +710,12 @@ __device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const S
             tld<8>(lanes + kTmO + c0 + c, o);
             tld_wait();
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              o[k] = __float_as_uint(__uint_as_float(o[k]) * fast_exp2(m[c + k] - raised(c + k)));
+            for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al[c0 + c + k]);
             tst8(lanes + kTmO + c0 + c, o);
           }
           tst_wait();
         }
-        mb ^= 1;
-        named_sync(bar_id, 128);                           // the new references are written, cm is free
-#pragma unroll
-        for (int c = 0; c < NC / 4; ++c) m4[c] = *reinterpret_cast<const float4*>(m_ref + mb * kMaxRows + c0 + 4 * c);
+        named_sync(bar_id, 128);                           // the factors are read
       }
       unsigned char* prow = sm + kPOff + (i % PB) * (kTileRows * PP) + row * PP;
       const int swz = PP == 128 ? row & 7 : (row >> 1) & 3;
@@ -764,7 +771,7 @@ __device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const S
         const int c = c0 + lane;
         const float t = cm[c] + cm[kMaxRows + c] + cm[2 * kMaxRows + c] + cm[3 * kMaxRows + c];
         float* rec = p.srec + (u.rec + c) * T::RS;
-        rec[0] = t == 0.f ? -INFINITY : m_ref[mb * kMaxRows + c];
+        rec[0] = t == 0.f ? -INFINITY : m_ref[c];
         rec[1] = t;
       }
     }
@@ -775,7 +782,7 @@ __device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const S
     // a bounded wait gave up: wait for what was issued, flag, poison the records
     if (tid == kMmaWarp * 32) {
       const bool drained = mbar_wait(bar(kBarDrain), 0, kShDrainSpin) &&
-                           (!u.load || mbar_wait(bar(kBarTab), 0, kShDrainSpin));
+                           (!u.load || (mbar_wait(bar(kBarTabK), 0, kShDrainSpin) && mbar_wait(bar(kBarTabV), 0, kShDrainSpin)));
       if (p.status != nullptr)
         atomicOr(p.status, drained ? LOOPVQ_DECODE_STATUS_TIMEOUT
                                    : (LOOPVQ_DECODE_STATUS_TIMEOUT | LOOPVQ_DECODE_STATUS_UNDRAINED));
@@ -812,9 +819,19 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_prefix_kernel(const Shar
                  "r"(kTmCols) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  // group g: first sequence, query rows, shared tokens, cost of its row tiles per head
+  // The walk: kept in shared memory by warp 0, so that the roles' loops have the
+  // registers to themselves.
+  struct Walk {
+    int64_t at, end, U, n;        // next cost, the block's last; all blocks' cost; blocks with work
+    int g, rt, pos, hkv;
+    int rows, tiles, S, lo;       // of group g
+    int head;                     // whose tables are in shared memory
+  };
+  Segment* seg = reinterpret_cast<Segment*>(sm + kSegOff);
+  Walk* walk = reinterpret_cast<Walk*>(sm + kSegOff + sizeof(Segment));
+  static_assert(sizeof(Segment) + sizeof(Walk) <= kTmemSlotOff - kSegOff, "segment and walk fit");
   struct Group {
-    int lo, rows, S, tiles, cost;
+    int lo, rows, S, tiles, cost; // cost: of its row tiles, per head
   };
   auto group = [&](int g) {
     Group r{0, 0, 0, 0, 0};
@@ -827,91 +844,113 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_prefix_kernel(const Shar
     }
     return r;
   };
-  // the cost of one head, and the group that cost `at` of it falls into (lane-uniform)
-  auto find = [&](int64_t at, int& g_out, int64_t& before) -> int64_t {
-    int64_t acc = 0;
-    g_out = -1;
-    before = 0;
-    for (int g0 = 0; g0 < p.n_groups; g0 += 32) {
-      const int cost = group(g0 + lane).cost;
-      int64_t incl = cost;
+  if (warp == 0) {
+    // the cost of one head, and the group that cost `x` of it falls into
+    auto find = [&](int64_t x, int& g_out, int64_t& before) -> int64_t {
+      int64_t acc = 0;
+      for (int g0 = 0; g0 < p.n_groups; g0 += 32) {
+        const int cost = group(g0 + lane).cost;
+        int64_t incl = cost;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t t = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += t;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t t = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += t;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, cost > 0 && x >= acc + incl - cost && x < acc + incl);
+        if (hit != 0u) {
+          const int src = __ffs(hit) - 1;
+          g_out = g0 + src;
+          before = acc + __shfl_sync(0xffffffffu, incl - cost, src);
+        }
+        acc += __shfl_sync(0xffffffffu, incl, 31);
       }
-      const unsigned hit = __ballot_sync(0xffffffffu, cost > 0 && at >= acc + incl - cost && at < acc + incl);
-      if (hit != 0u) {
-        const int src = __ffs(hit) - 1;
-        g_out = g0 + src;
-        before = acc + __shfl_sync(0xffffffffu, incl - cost, src);
-      }
-      acc += __shfl_sync(0xffffffffu, incl, 31);
+      return acc;
+    };
+    Walk w{};
+    int64_t before = 0;
+    const int64_t Ug = find(-1, w.g, before);
+    w.U = Ug * p.Hkv;
+    w.n = min(static_cast<int64_t>(gridDim.x), w.U);
+    w.head = -1;
+    if (blockIdx.x < w.n) {
+      w.at = w.U * blockIdx.x / w.n;
+      w.end = w.U * (blockIdx.x + 1) / w.n;
+      w.hkv = static_cast<int>(w.at / Ug);
+      const int64_t x = w.at - w.hkv * Ug;
+      find(x, w.g, before);
+      const Group r = group(w.g);
+      const int off = static_cast<int>(x - before), cost = r.tiles + kSetupTiles;
+      w.rt = off / cost;
+      w.pos = off - w.rt * cost;
+      w.lo = r.lo;
+      w.rows = r.rows;
+      w.S = r.S;
+      w.tiles = r.tiles;
     }
-    return acc;
-  };
-  int g = 0;
-  int64_t before;
-  const int64_t Ug = find(-1, g, before), U = Ug * p.Hkv;
-  const int64_t n = min(static_cast<int64_t>(gridDim.x), U);   // blocks with work
+    if (lane == 0) *walk = w;
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");       // the tables are written
   asm volatile("griddepcontrol.launch_dependents;");       // ... so the own grid may start
   tc_before();
   __syncthreads();
   tc_after();
   const uint32_t tmem = *tmem_slot;
-  if (blockIdx.x < n) {                                    // block-uniform
-    int64_t at = U * blockIdx.x / n;
-    const int64_t end = U * (blockIdx.x + 1) / n;
-    int hkv = static_cast<int>(at / Ug), head_in_smem = -1;
-    find(at - hkv * Ug, g, before);
-    Group r = group(g);
-    int64_t off = at - hkv * Ug - before;
-    int rt = static_cast<int>(off / (r.tiles + kSetupTiles)), pos = static_cast<int>(off % (r.tiles + kSetupTiles));
-    bool ok = true;
-    while (at < end) {
-      const int cost = r.tiles + kSetupTiles;
-      const int take = static_cast<int>(min(static_cast<int64_t>(cost - pos), end - at));
+  bool ok = true;
+  while (walk->at < walk->end) {                           // block-uniform
+    if (tid == 0) {
+      const Walk w = *walk;
+      const int cost = w.tiles + kSetupTiles, take = static_cast<int>(min(static_cast<int64_t>(cost - w.pos), w.end - w.at));
       Segment u;
-      u.g = g;
-      u.rt = rt;
-      u.hkv = hkv;
-      u.lo = r.lo;
-      u.rows = min(r.rows - rt * N, N);
-      u.S = r.S;
-      u.tile0 = max(pos - kSetupTiles, 0);
-      u.nt = max(pos + take - kSetupTiles, 0) - u.tile0;
-      const int64_t R = (static_cast<int64_t>(hkv) * p.B + r.lo) * p.ratio + rt * N;
-      u.rec = R + static_cast<int64_t>(blockIdx.x) * N;
-      u.load = hkv != head_in_smem;
-      if (pos == 0) {                                      // the unit's first block: where its rows' records are
-        const int64_t c0 = ((at + 1) * n - 1) / U, c1 = ((at + cost) * n - 1) / U;
-        for (int c = tid; c < u.rows; c += kShThreads)
-          p.spans[pair_of<N>(p, u, c)] = make_int2(static_cast<int>(R + c0 * N + c), static_cast<int>(c1 - c0 + 1));
-      }
-      if (u.nt > 0 && ok) {
-        ok = shared_segment<J, C, N>(p, sm, u, tmem);
-        head_in_smem = hkv;
-      }
-      if (u.nt <= 0 || !ok) {                              // no tiles, or given up
-        for (int c = tid; c < u.rows; c += kShThreads) {
-          p.srec[(u.rec + c) * T::RS] = ok ? -INFINITY : NAN;
-          p.srec[(u.rec + c) * T::RS + 1] = ok ? 0.f : 1.f;
-        }
-      }
-      at += take;
-      pos = 0;
-      if (++rt * N >= r.rows) {                            // next group with shared tokens, next head
-        rt = 0;
-        do {
-          if (++g == p.n_groups) {
-            g = 0;
-            ++hkv;
-          }
-          r = group(g);
-        } while (r.cost == 0 && at < end);
+      u.hkv = w.hkv;
+      u.rt = w.rt;
+      u.lo = w.lo;
+      u.rows = min(w.rows - w.rt * N, N);
+      u.S = w.S;
+      u.tile0 = max(w.pos - kSetupTiles, 0);
+      u.nt = max(w.pos + take - kSetupTiles, 0) - u.tile0;
+      u.rec = (static_cast<int64_t>(w.hkv) * p.B + w.lo) * p.ratio + w.rt * N + static_cast<int64_t>(blockIdx.x) * N;
+      u.load = w.hkv != w.head;
+      *seg = u;
+      if (u.nt > 0) walk->head = w.hkv;
+    }
+    __syncthreads();
+    if (walk->pos == 0) {                                  // the unit's first block: where its rows' records are
+      const int64_t at = walk->at, n = walk->n, U = walk->U;
+      const int64_t c0 = ((at + 1) * n - 1) / U, c1 = ((at + walk->tiles + kSetupTiles) * n - 1) / U;
+      for (int c = tid; c < seg->rows; c += kShThreads)
+        p.spans[pair_of<N>(p, *seg, c)] =
+            make_int2(static_cast<int>(seg->rec + (c0 - blockIdx.x) * N + c), static_cast<int>(c1 - c0 + 1));
+    }
+    if (seg->nt > 0 && ok) ok = shared_segment<J, C, N>(p, sm, *seg, tmem);
+    if (seg->nt <= 0 || !ok) {                             // no tiles, or given up
+      for (int c = tid; c < seg->rows; c += kShThreads) {
+        p.srec[(seg->rec + c) * T::RS] = ok ? -INFINITY : NAN;
+        p.srec[(seg->rec + c) * T::RS + 1] = ok ? 0.f : 1.f;
       }
     }
+    __syncthreads();                                       // the segment is read
+    if (tid == 0) {                                        // next row tile, group with shared tokens, head
+      Walk w = *walk;
+      w.at += min(static_cast<int64_t>(w.tiles + kSetupTiles - w.pos), w.end - w.at);
+      w.pos = 0;
+      if (++w.rt * N >= w.rows && w.at < w.end) {
+        w.rt = 0;
+        Group r;
+        do {
+          if (++w.g == p.n_groups) {
+            w.g = 0;
+            ++w.hkv;
+          }
+          r = group(w.g);
+        } while (r.cost == 0);
+        w.lo = r.lo;
+        w.rows = r.rows;
+        w.S = r.S;
+        w.tiles = r.tiles;
+      }
+      *walk = w;
+    }
+    __syncthreads();
   }
   tc_before();
   __syncthreads();
@@ -962,7 +1001,7 @@ __device__ __forceinline__ void axpy_f16(float& x, float& y, uint32_t w, uint32_
 }
 
 // bf16 window of (b, hkv): lane = 4 channels, D/4 lanes a token (two tokens side
-// by side at D = 64), eight steps of rows requested ahead of their sums. The
+// by side at D = 64), rows requested two steps of eight ahead of their sums. The
 // scores of eight tokens are summed over the lanes together, half of them
 // changing lanes at each of the first three exchanges.
 template <int D>
@@ -974,19 +1013,17 @@ __device__ void own_window(const SharedParams& p, int64_t head, int n_win, const
   const uint16_t* wk = p.win_k + head * p.W * D + 4 * c4;
   const uint16_t* wv = p.win_v + head * p.W * D + 4 * c4;
   float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  uint2 kr[U], vr[U];
-  auto request = [&](int n0) {
+  uint2 kr[2][U], vr[2][U];
+  auto request = [&](int n0, uint2 (&k)[U], uint2 (&v)[U]) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int n = n0 + u * SIDES + side;
       const bool ok = act && n < n_win;
-      kr[u] = ok ? __ldg(reinterpret_cast<const uint2*>(wk + static_cast<int64_t>(n) * D)) : make_uint2(0u, 0u);
-      vr[u] = ok ? __ldg(reinterpret_cast<const uint2*>(wv + static_cast<int64_t>(n) * D)) : make_uint2(0u, 0u);
+      k[u] = ok ? __ldg(reinterpret_cast<const uint2*>(wk + static_cast<int64_t>(n) * D)) : make_uint2(0u, 0u);
+      v[u] = ok ? __ldg(reinterpret_cast<const uint2*>(wv + static_cast<int64_t>(n) * D)) : make_uint2(0u, 0u);
     }
   };
-  request(0);
-#pragma unroll 1
-  for (int n0 = 0; n0 < n_win; n0 += U * SIDES) {
+  auto step = [&](int n0, uint2 (&kr)[U], uint2 (&vr)[U]) {
     float x[U];
     uint2 v[U];
 #pragma unroll
@@ -996,7 +1033,7 @@ __device__ void own_window(const SharedParams& p, int64_t head, int n_win, const
       dot_bf16(x[u], q.y, kr[u].y);
       v[u] = vr[u];
     }
-    if (n0 + U * SIDES < n_win) request(n0 + U * SIDES);
+    request(n0 + 2 * U * SIDES, kr, vr);                   // (past the window: nothing)
 #pragma unroll
     for (int h = U / 2, off = LN / 2; h >= 1; h >>= 1, off >>= 1) {
       const bool up = (lane & off) != 0;
@@ -1030,6 +1067,13 @@ __device__ void own_window(const SharedParams& p, int64_t head, int n_win, const
       o[2] = fmaf(wu, b.x, o[2]);
       o[3] = fmaf(wu, b.y, o[3]);
     }
+  };
+  request(0, kr[0], vr[0]);
+  request(U * SIDES, kr[1], vr[1]);
+#pragma unroll 1
+  for (int n0 = 0; n0 < n_win; n0 += 2 * U * SIDES) {
+    step(n0, kr[0], vr[0]);
+    if (n0 + U * SIDES < n_win) step(n0 + U * SIDES, kr[1], vr[1]);
   }
   l = warp_sum(l);
   if constexpr (SIDES == 2) {
@@ -1206,7 +1250,7 @@ __global__ void __launch_bounds__(kOwnWarps * 32, 1) shared_own_kernel(const Sha
     return;
   }
   if (tid == 0) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(1u) : "memory");
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(2u) : "memory");
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
@@ -1216,17 +1260,18 @@ __global__ void __launch_bounds__(kOwnWarps * 32, 1) shared_own_kernel(const Sha
   uint32_t* qs = reinterpret_cast<uint32_t*>(scratch + kOwnQ);
   // tasks (head, sequence, query head of it, window or chunk), heads outermost; the
   // block takes its share of the list, one or a few heads
-  const int64_t per_head = static_cast<int64_t>(p.B) * p.ratio * p.NC;
-  const int64_t t_lo = per_head * p.Hkv * blockIdx.x / gridDim.x, t_hi = per_head * p.Hkv * (blockIdx.x + 1) / gridDim.x;
+  const int per_head = p.B * p.ratio * p.NC;               // (times Hkv below 2^31: checked on the host)
+  const int t_lo = static_cast<int>(static_cast<int64_t>(per_head) * p.Hkv * blockIdx.x / gridDim.x);
+  const int t_hi = static_cast<int>(static_cast<int64_t>(per_head) * p.Hkv * (blockIdx.x + 1) / gridDim.x);
   bool failed = false;
   int phase = 0;
-  for (int64_t th = t_lo; th < t_hi; ++phase) {            // block-uniform
-   const int hkv = static_cast<int>(th / per_head);
-   const int64_t t_end = min(t_hi, (hkv + 1) * per_head);
+  for (int th = t_lo; th < t_hi; ++phase) {            // block-uniform
+   const int hkv = th / per_head;
+   const int t_end = min(t_hi, (hkv + 1) * per_head);
    const int* exk = p.exps + hkv * 64;
    if (!failed) {
     __syncthreads();                                       // the head before is done with tables and scales
-    if (tid == 0) request_tables(p, sm, hkv, bar);
+    if (tid < 2) request_table(p, sm, hkv, tid, bar);
     if (tid < J) fk[tid] = ldexpf(1.f, -__ldg(exk + tid));
     failed = __syncthreads_or(!mbar_wait(bar, phase & 1, kShSpin));
     if (failed && tid == 0) {                              // no copy may outlive the block
@@ -1238,11 +1283,10 @@ __global__ void __launch_bounds__(kOwnWarps * 32, 1) shared_own_kernel(const Sha
    }
    const float unv = lane < J ? ldexpf(1.f, -__ldg(exk + 32 + lane)) : 0.f;   // of this lane's record channels
    const uint8_t* pool_h = p.pool_lg + hkv * p.pool_stride_head;
-   for (int64_t ti = th + warp; ti < t_end; ti += kOwnWarps) {
-    const int64_t t = ti - hkv * per_head;
-    const int ck = static_cast<int>(t % p.NC) - 1;         // -1: the window
-    const int64_t y = t / p.NC;
-    const int r = static_cast<int>(y % p.ratio), b = static_cast<int>(y / p.ratio);
+   for (int ti = th + warp; ti < t_end; ti += kOwnWarps) {
+    const int t = ti - hkv * per_head;
+    const int y = t / p.NC, ck = t - y * p.NC - 1;         // -1: the window
+    const int b = y / p.ratio, r = y - b * p.ratio;
     const int64_t pair = static_cast<int64_t>(b) * p.Hq + hkv * p.ratio + r;
     float* rec = p.orec + (pair * p.NC + ck + 1) * T::RS;
     if (failed) {
@@ -1363,18 +1407,24 @@ SharedPlan make_plan(const Geometry& g, int batch, int n_groups, int max_group, 
   // measured: a tile, a unit's setup, an own or window token).
   const double t_tile = q.N > 32 ? 3300 : 2100, t_token = 13;
   const int tiles = (max_shared + 4 * g.LB - 1) / (4 * g.LB);
-  const double units = max_shared > 0 ? (static_cast<double>(batch) * ratio / q.N + n_groups) * g.Hkv : 0;
+  const int64_t tiles_of_rows = n_groups * ((rows + q.N - 1) / q.N), by_batch = n_groups + static_cast<int64_t>(batch) * ratio / q.N;
+  const double units = max_shared > 0 ? static_cast<double>(tiles_of_rows < by_batch ? tiles_of_rows : by_batch) * g.Hkv : 0;
   const double work_a = units * (tiles + 5) * t_tile;
   const double work_b = static_cast<double>(batch) * g.Hq * (max_own * 0.75 + g.W) * t_token;
   const int64_t tasks = static_cast<int64_t>(batch) * g.Hq * q.NC;
   const int64_t most_b = (tasks + 15) / 16;
-  int64_t nb = static_cast<int64_t>(kPlanSms * work_b / (work_a + work_b) + 0.5);
-  nb = nb < 1 ? 1 : nb;
+  double nb = kPlanSms * work_b / (work_a + work_b) + 0.5;
+  // ... and the own grid's warps, each through its tasks one after the other (15
+  // thousand cycles of latency each), are done no later than the shared grid
+  const double lat = 1.25 * tasks / 16 * 15000 / (work_a / kPlanSms + 20000);
+  if (lat > nb) nb = lat;
+  if (nb < 1) nb = 1;
+  if (units > 0 && nb > kPlanSms / 2 && nb > kPlanSms * work_b / (work_a + work_b)) nb = kPlanSms * work_b / (work_a + work_b) + 1;
   if (units > 0 && nb > kPlanSms - 1) nb = kPlanSms - 1;
   q.own_blocks = static_cast<int>(nb < most_b ? nb : most_b);
   if (units > 0) {
     const double most_a = units * tiles;
-    const int na = kPlanSms - static_cast<int>(nb);
+    const int na = kPlanSms - q.own_blocks;
     q.shared_blocks = most_a < na ? static_cast<int>(most_a) : na;
   }
   return q;
@@ -1483,8 +1533,8 @@ size_t shared_attn_workspace_bytes(const Geometry& g, int batch, int n_groups, i
 loopvq_status launch_shared_attn(const SharedArgs& a) {
   const Geometry& g = *a.geo;
   const SharedPlan q = make_plan(g, a.batch, a.n_groups, a.max_group, a.max_shared, a.max_own);
-  // (records are counted in 32 bits)
-  if (static_cast<int64_t>(a.batch) * g.Hq > INT_MAX / 2) return LOOPVQ_ERR_UNSUPPORTED;
+  // (records and tasks are counted in 32 bits)
+  if (static_cast<int64_t>(a.batch) * g.Hq * q.NC > INT_MAX / 2) return LOOPVQ_ERR_UNSUPPORTED;
   const int gamma = a.loop_step / g.g, tau = a.loop_step % g.g;
   SharedParams p{};
   p.q = static_cast<const uint16_t*>(a.q);
