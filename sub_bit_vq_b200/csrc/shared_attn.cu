@@ -97,7 +97,7 @@ constexpr int kNvOff = kLimOff + kMaxRows * 4;             // int [4 tiles][4 bl
 constexpr int kRedOff = kNvOff + 64;                       // float [25]: block reduction
 constexpr int kBarOff = kRedOff + 112;                     // mbarriers
 constexpr int kSegOff = kBarOff + 96;                      // the block's segment and walk
-constexpr int kTmemSlotOff = kSegOff + 112;
+constexpr int kTmemSlotOff = kSegOff + 144;
 constexpr int kShSmem = kTmemSlotOff + 16;
 static_assert(kShSmem <= 227 * 1024, "shared memory above 227 KB");
 
@@ -107,6 +107,16 @@ enum { kBarK = 0, kBarV, kBarS0, kBarS1, kBarP0, kBarP1, kBarO0, kBarO1, kBarTab
 static_assert(kBars * 8 <= kTmemSlotOff - kBarOff, "barriers fit");
 
 constexpr uint32_t kTmCols = 256, kTmS = 0, kTmO = 128;    // TMEM columns: S^T twice 64, O^T 64
+
+// Where a block of the shared grid is in the list of units: see
+// shared_prefix_kernel.
+struct Walk {
+  int64_t at, end, U, n;          // next cost, the block's last; all blocks' cost; blocks with work
+  int g, rt, pos, hkv;            // group, row tile, cost inside the unit, head
+  int rows, tiles, S, lo;         // of group g: query rows, shared tiles and tokens, first sequence
+  int head, pad[3];               // whose tables are in shared memory
+};
+static_assert(sizeof(Walk) % 16 == 0, "copied by 16 bytes");
 
 struct SharedParams {
   const uint16_t* q;              // bf16 [B][Hq][d]
@@ -131,6 +141,7 @@ struct SharedParams {
   float* lse;
   int B, n_groups, Hq, Hkv, ratio, W, Pg, n_pages, max_pages_per_seq;
   int max_group, max_shared, max_own;
+  Walk* walks;                    // [shared_blocks] where each block starts
   int2* spans;                    // [pairs] first shared record of a row, and their number (N records apart)
   int NC, CH;                     // own records of a pair (window, chunks), tokens of a chunk
   int shared_blocks, own_blocks;  // grids
@@ -298,11 +309,96 @@ __device__ __forceinline__ int group_shared(const SharedParams& p, int g) {
   return max(0, min(__ldg(p.shared_lens + g), p.max_shared));
 }
 
+// Tokens of the tensor-core setup of a unit, in tiles: what a block that starts
+// a unit spends on its tables, queries, first tile and records.
+constexpr int kSetupTiles = 5;
+
+struct Group {
+  int lo, rows, S, tiles, cost;   // first sequence, query rows, shared tokens and tiles, cost of its row tiles per head
+};
+template <int TOK, int N>
+__device__ __forceinline__ Group group_info(const SharedParams& p, int g) {
+  Group r{0, 0, 0, 0, 0};
+  if (g < p.n_groups) {
+    r.lo = max(0, __ldg(p.group_starts + g));
+    r.rows = max(0, min(min(p.B, __ldg(p.group_starts + g + 1)) - r.lo, p.max_group)) * p.ratio;
+    r.S = group_shared(p, g);
+    r.tiles = (r.S + TOK - 1) / TOK;
+    r.cost = r.tiles > 0 ? (r.rows + N - 1) / N * (r.tiles + kSetupTiles) : 0;
+  }
+  return r;
+}
+
+// Where every block of the shared grid starts (one block of kE threads).
+template <int TOK, int N>
+__device__ void plan_walks(const SharedParams& p) {
+  __shared__ int64_t incl[kE];
+  __shared__ int64_t part[kE / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // inclusive sums of the costs of groups g0 .. g0 + kE - 1 into incl
+  auto scan = [&](int g0) {
+    int64_t v = group_info<TOK, N>(p, g0 + tid).cost;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t t = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += t;
+    }
+    __syncthreads();
+    if (lane == 31) part[warp] = v;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) v += part[w];
+    incl[tid] = v;
+    __syncthreads();
+  };
+  int64_t Ug = 0;
+  for (int g0 = 0; g0 < p.n_groups; g0 += kE) {
+    scan(g0);
+    Ug += incl[kE - 1];
+  }
+  const int64_t U = Ug * p.Hkv, n = min(static_cast<int64_t>(p.shared_blocks), U);
+  for (int c0 = 0; c0 < p.shared_blocks; c0 += kE) {
+    const int c = c0 + tid;
+    Walk w{};
+    w.U = U;
+    w.n = n;
+    w.head = -1;
+    int64_t x = -1;
+    if (c < n) {
+      w.at = U * c / n;
+      w.end = U * (c + 1) / n;
+      w.hkv = static_cast<int>(w.at / Ug);
+      x = w.at - w.hkv * Ug;
+    }
+    int64_t before = 0;                                    // cost of the groups before g0
+    for (int g0 = 0; g0 < p.n_groups; g0 += kE) {
+      if (p.n_groups > kE) scan(g0);                       // (else incl still holds the only sums)
+      if (x >= before && x < before + incl[kE - 1]) {
+        int a = 0, z = kE - 1;                             // first group whose inclusive sum passes x
+        while (a < z) {
+          const int mid = (a + z) / 2;
+          if (before + incl[mid] > x) z = mid; else a = mid + 1;
+        }
+        const Group r = group_info<TOK, N>(p, g0 + a);
+        const int off = static_cast<int>(x - before - (a > 0 ? incl[a - 1] : 0)), cost = r.tiles + kSetupTiles;
+        w.g = g0 + a;
+        w.rt = off / cost;
+        w.pos = off - w.rt * cost;
+        w.lo = r.lo;
+        w.rows = r.rows;
+        w.S = r.S;
+        w.tiles = r.tiles;
+      }
+      before += incl[kE - 1];
+    }
+    if (c < p.shared_blocks) p.walks[c] = w;
+  }
+}
+
 // The codebook slices of one call as fp16 tables: block (4 channel groups, K or
 // V, head), thread = codeword. Each group is scaled by a power of two of its
-// own. Also the split of every sequence into shared and own tokens. Blocks of the
-// attention grid start meanwhile and wait for this grid.
-template <int J, int C>
+// own. Also the split of every sequence into shared and own tokens and, in a block
+// of its own, where the shared grid's blocks start. Blocks of the attention grid start meanwhile and wait for this grid.
+template <int J, int C, int N>
 __global__ void __launch_bounds__(kE) shared_table_kernel(const float* cb_k, const float* cb_v, int64_t cb_stride_head,
                                                           unsigned char* tables, int* exps, const SharedParams p) {
   __shared__ float red[4][kE / 32];
@@ -323,6 +419,10 @@ __global__ void __launch_bounds__(kE) shared_table_kernel(const float* cb_k, con
         if (n_own < n_vq - s0 && p.status != nullptr) atomicOr(p.status, LOOPVQ_DECODE_STATUS_BAD_GROUP);
       }
     }
+  }
+  if (blockIdx.z == static_cast<unsigned>(p.Hkv)) {
+    if (blockIdx.x == 0 && blockIdx.y == 0 && p.shared_blocks > 0) plan_walks<Shape<J, C>::TOK, N>(p);
+    return;
   }
   const int j0 = blockIdx.x * 4, kv = blockIdx.y, h = blockIdx.z, e = threadIdx.x;
   const float* cb = (kv ? cb_v : cb_k) + h * cb_stride_head;
@@ -410,6 +510,7 @@ struct Segment {
   int S, tile0, nt;               // shared tokens of the group, tiles [tile0, tile0 + nt)
   int load;                       // the head's tables are not in shared memory yet
   int64_t rec;                    // record of row 0
+  int64_t pad;
 };
 
 // Query row c of the unit as (sequence, query head).
@@ -795,10 +896,6 @@ __device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const S
   return !any_failed;
 }
 
-// Tokens of the tensor-core setup of a unit, in tiles: what a block that starts
-// a unit spends on its tables, queries, first tile and records.
-constexpr int kSetupTiles = 5;
-
 // A persistent grid over the tiles of all units, heads outermost. A unit counts
 // kSetupTiles + its tiles; block c of n takes the c-th n-th of the total U, so
 // every block does the same work whatever the groups' sizes and lengths, and
@@ -812,85 +909,22 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_prefix_kernel(const Shar
     if (threadIdx.x == 0 && p.status != nullptr) atomicOr(p.status, LOOPVQ_DECODE_STATUS_SHARED_BASE);
     return;
   }
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = tid >> 5;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kTmemSlotOff);
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(u32s(tmem_slot)),
                  "r"(kTmCols) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  // The walk: kept in shared memory by warp 0, so that the roles' loops have the
-  // registers to themselves.
-  struct Walk {
-    int64_t at, end, U, n;        // next cost, the block's last; all blocks' cost; blocks with work
-    int g, rt, pos, hkv;
-    int rows, tiles, S, lo;       // of group g
-    int head;                     // whose tables are in shared memory
-  };
+  // The walk is kept in shared memory, so that the roles' loops have the registers
+  // to themselves.
   Segment* seg = reinterpret_cast<Segment*>(sm + kSegOff);
   Walk* walk = reinterpret_cast<Walk*>(sm + kSegOff + sizeof(Segment));
-  static_assert(sizeof(Segment) + sizeof(Walk) <= kTmemSlotOff - kSegOff, "segment and walk fit");
-  struct Group {
-    int lo, rows, S, tiles, cost; // cost: of its row tiles, per head
-  };
-  auto group = [&](int g) {
-    Group r{0, 0, 0, 0, 0};
-    if (g < p.n_groups) {
-      r.lo = max(0, __ldg(p.group_starts + g));
-      r.rows = max(0, min(min(p.B, __ldg(p.group_starts + g + 1)) - r.lo, p.max_group)) * p.ratio;
-      r.S = group_shared(p, g);
-      r.tiles = (r.S + T::TOK - 1) / T::TOK;
-      r.cost = r.tiles > 0 ? (r.rows + N - 1) / N * (r.tiles + kSetupTiles) : 0;
-    }
-    return r;
-  };
-  if (warp == 0) {
-    // the cost of one head, and the group that cost `x` of it falls into
-    auto find = [&](int64_t x, int& g_out, int64_t& before) -> int64_t {
-      int64_t acc = 0;
-      for (int g0 = 0; g0 < p.n_groups; g0 += 32) {
-        const int cost = group(g0 + lane).cost;
-        int64_t incl = cost;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t t = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += t;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, cost > 0 && x >= acc + incl - cost && x < acc + incl);
-        if (hit != 0u) {
-          const int src = __ffs(hit) - 1;
-          g_out = g0 + src;
-          before = acc + __shfl_sync(0xffffffffu, incl - cost, src);
-        }
-        acc += __shfl_sync(0xffffffffu, incl, 31);
-      }
-      return acc;
-    };
-    Walk w{};
-    int64_t before = 0;
-    const int64_t Ug = find(-1, w.g, before);
-    w.U = Ug * p.Hkv;
-    w.n = min(static_cast<int64_t>(gridDim.x), w.U);
-    w.head = -1;
-    if (blockIdx.x < w.n) {
-      w.at = w.U * blockIdx.x / w.n;
-      w.end = w.U * (blockIdx.x + 1) / w.n;
-      w.hkv = static_cast<int>(w.at / Ug);
-      const int64_t x = w.at - w.hkv * Ug;
-      find(x, w.g, before);
-      const Group r = group(w.g);
-      const int off = static_cast<int>(x - before), cost = r.tiles + kSetupTiles;
-      w.rt = off / cost;
-      w.pos = off - w.rt * cost;
-      w.lo = r.lo;
-      w.rows = r.rows;
-      w.S = r.S;
-      w.tiles = r.tiles;
-    }
-    if (lane == 0) *walk = w;
-  }
+  static_assert(sizeof(Segment) % 16 == 0 && sizeof(Segment) + sizeof(Walk) <= kTmemSlotOff - kSegOff, "segment and walk fit");
   asm volatile("griddepcontrol.wait;" ::: "memory");       // the tables are written
   asm volatile("griddepcontrol.launch_dependents;");       // ... so the own grid may start
+  if (tid < static_cast<int>(sizeof(Walk) / 16))
+    reinterpret_cast<uint4*>(walk)[tid] = __ldcg(reinterpret_cast<const uint4*>(p.walks + blockIdx.x) + tid);
   tc_before();
   __syncthreads();
   tc_after();
@@ -914,19 +948,19 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_prefix_kernel(const Shar
       if (u.nt > 0) walk->head = w.hkv;
     }
     __syncthreads();
-    if (walk->pos == 0) {                                  // the unit's first block: where its rows' records are
-      const int64_t at = walk->at, n = walk->n, U = walk->U;
-      const int64_t c0 = ((at + 1) * n - 1) / U, c1 = ((at + walk->tiles + kSetupTiles) * n - 1) / U;
-      for (int c = tid; c < seg->rows; c += kShThreads)
-        p.spans[pair_of<N>(p, *seg, c)] =
-            make_int2(static_cast<int>(seg->rec + (c0 - blockIdx.x) * N + c), static_cast<int>(c1 - c0 + 1));
-    }
     if (seg->nt > 0 && ok) ok = shared_segment<J, C, N>(p, sm, *seg, tmem);
     if (seg->nt <= 0 || !ok) {                             // no tiles, or given up
       for (int c = tid; c < seg->rows; c += kShThreads) {
         p.srec[(seg->rec + c) * T::RS] = ok ? -INFINITY : NAN;
         p.srec[(seg->rec + c) * T::RS + 1] = ok ? 0.f : 1.f;
       }
+    }
+    if (walk->pos == 0) {                                  // the unit's first block: where its rows' records are
+      const int64_t at = walk->at, n = walk->n, U = walk->U;
+      const int64_t c0 = ((at + 1) * n - 1) / U, c1 = ((at + walk->tiles + kSetupTiles) * n - 1) / U;
+      for (int c = tid; c < seg->rows; c += kShThreads)
+        p.spans[pair_of<N>(p, *seg, c)] =
+            make_int2(static_cast<int>(seg->rec + (c0 - blockIdx.x) * N + c), static_cast<int>(c1 - c0 + 1));
     }
     __syncthreads();                                       // the segment is read
     if (tid == 0) {                                        // next row tile, group with shared tokens, head
@@ -941,7 +975,7 @@ __global__ void __launch_bounds__(kShThreads, 1) shared_prefix_kernel(const Shar
             w.g = 0;
             ++w.hkv;
           }
-          r = group(w.g);
+          r = group_info<T::TOK, N>(p, w.g);
         } while (r.cost == 0);
         w.lo = r.lo;
         w.rows = r.rows;
@@ -1480,9 +1514,9 @@ loopvq_status launch_shared_jc(const SharedParams& p, int N, cudaStream_t st) {
   static std::atomic<uint64_t> configured{0};
   loopvq_status s = configure(shared_own_kernel<J, C>, kOwnSmem, configured);
   if (s != LOOPVQ_OK) return s;
-  shared_table_kernel<J, C><<<dim3(J / 4, 2, p.Hkv), kE, 0, st>>>(p.cb_k, p.cb_v, p.cb_stride_head,
-                                                                  const_cast<unsigned char*>(p.tables),
-                                                                  const_cast<int*>(p.exps), p);
+  auto tables = N == 16 ? shared_table_kernel<J, C, 16> : N == 32 ? shared_table_kernel<J, C, 32> : shared_table_kernel<J, C, 64>;
+  tables<<<dim3(J / 4, 2, p.Hkv + 1), kE, 0, st>>>(p.cb_k, p.cb_v, p.cb_stride_head, const_cast<unsigned char*>(p.tables),
+                                                   const_cast<int*>(p.exps), p);
   if (cudaGetLastError() != cudaSuccess) return LOOPVQ_ERR_CUDA;
   if (p.shared_blocks > 0) {
     s = N == 16 ? launch_prefix<J, C, 16>(p, st) : N == 32 ? launch_prefix<J, C, 32>(p, st) : launch_prefix<J, C, 64>(p, st);
@@ -1500,7 +1534,7 @@ loopvq_status launch_shared_jc(const SharedParams& p, int N, cudaStream_t st) {
 
 // Byte offsets of the workspace's parts.
 struct SharedLayout {
-  size_t srec, orec, tables, exps, spans, seqs, end;
+  size_t srec, orec, tables, exps, walks, spans, seqs, end;
 };
 SharedLayout make_layout(const Geometry& g, int batch, const SharedPlan& q) {
   const size_t rec = (4 + static_cast<size_t>(g.d)) * sizeof(float), pairs = static_cast<size_t>(batch) * g.Hq;
@@ -1509,7 +1543,8 @@ SharedLayout make_layout(const Geometry& g, int batch, const SharedPlan& q) {
   w.orec = w.srec + (q.shared_blocks > 0 ? pairs + static_cast<size_t>(q.shared_blocks) * q.N : 0) * rec;
   w.tables = w.orec + pairs * q.NC * rec;
   w.exps = w.tables + static_cast<size_t>(g.Hkv) * 2 * kTabBytes;
-  w.spans = w.exps + static_cast<size_t>(g.Hkv) * 64 * sizeof(int);
+  w.walks = w.exps + static_cast<size_t>(g.Hkv) * 64 * sizeof(int);
+  w.spans = w.walks + static_cast<size_t>(q.shared_blocks) * sizeof(Walk);
   w.seqs = w.spans + pairs * sizeof(int2);
   w.end = w.seqs + static_cast<size_t>(batch) * sizeof(int2);
   return w;
@@ -1558,6 +1593,7 @@ loopvq_status launch_shared_attn(const SharedArgs& a) {
   p.orec = reinterpret_cast<float*>(ws + w.orec);
   p.tables = reinterpret_cast<unsigned char*>(ws + w.tables);
   p.exps = reinterpret_cast<int*>(ws + w.exps);
+  p.walks = reinterpret_cast<Walk*>(ws + w.walks);
   p.spans = reinterpret_cast<int2*>(ws + w.spans);
   p.seqs = reinterpret_cast<int2*>(ws + w.seqs);
   p.out = a.out;
