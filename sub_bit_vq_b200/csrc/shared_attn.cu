@@ -182,9 +182,13 @@ __device__ __forceinline__ uint32_t idesc_f16(int n, uint32_t ta, uint32_t tb) {
   return (1u << 4) | (ta << 15) | (tb << 16) | ((static_cast<uint32_t>(n) >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-// Byte offset of (row, byte of the row) in a tile: groups of 8 rows, each two
-// channel blocks of 8 x 128 bytes, 16-byte pieces swizzled by the row.
+// Byte offset of (row, byte of the row) in a tile: groups of 8 rows, 2 KB each.
+// 8-byte entries: two channel blocks of 8 x 128 bytes, 16-byte pieces swizzled by
+// the row. 16-byte entries: pieces of 8 rows x 16 bytes without a swizzle (the
+// rotation of the rows would undo it: lane i writes group s + i of row i).
+template <int ENTRY>
 __device__ __forceinline__ uint32_t tile_off(int row, int byte) {
+  if constexpr (ENTRY == 16) return static_cast<uint32_t>((row >> 3) * 2048 + (byte >> 4) * 128 + (row & 7) * 16);
   return static_cast<uint32_t>((row >> 3) * 2048 + (byte >> 7) * 1024 + (row & 7) * 128 +
                                (((byte & 127) & ~15) ^ ((row & 7) << 4)) + (byte & 15));
 }
@@ -617,7 +621,7 @@ __device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const S
 #pragma unroll
     for (int w = 0; w < 4 * W0; ++w) {
       const int j = (w_first * 4 + w + lane) % J;
-      at[w] = static_cast<uint32_t>(j * T::ENTRY) | (tile_off(row, j * T::ENTRY) << 16);
+      at[w] = static_cast<uint32_t>(j * T::ENTRY) | (tile_off<T::ENTRY>(row, j * T::ENTRY) << 16);
     }
     // this lane's row in block 0 of page 0 (granule of its first word)
     const uint8_t* rows0 = p.pool_lg + hkv * p.pool_stride_head + (values ? p.plane_bytes : 0) + lane * T::GR +
@@ -692,16 +696,19 @@ __device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const S
     if (lane == 0) {
       // descriptors: the high words are constant, the low words the address plus
       // an immediate
-      const uint32_t k_hi = desc_hi(2048, kSw128), q_hi = desc_hi(1024, kSw128), v_hi = desc_hi(2048, kSw128);
+      // (K along the channels, V along the tokens; see tile_off for the two layouts)
+      constexpr bool SW = T::ENTRY == 8;
+      const uint32_t k_hi = desc_hi(2048, SW ? kSw128 : 0u), q_hi = desc_hi(1024, kSw128);
+      const uint32_t v_hi = SW ? desc_hi(2048, kSw128) : desc_hi(128, 0u);
       const uint32_t p_hi = desc_hi(PP * 8, PP == 128 ? kSw128 : kSw64);
-      const uint32_t k_lo = desc_lo(u32s(sm + kKtileOff), 16), q_lo = desc_lo(u32s(sm + kQOff), 16);
-      const uint32_t v_lo = desc_lo(u32s(sm + kVtileOff), 1024), p_lo = desc_lo(u32s(sm + kPOff), 16);
+      const uint32_t k_lo = desc_lo(u32s(sm + kKtileOff), SW ? 16 : 128), q_lo = desc_lo(u32s(sm + kQOff), 16);
+      const uint32_t v_lo = desc_lo(u32s(sm + kVtileOff), SW ? 1024 : 2048), p_lo = desc_lo(u32s(sm + kPOff), 16);
       auto product_s = [&](int i) {                        // S^T of tile i
         tc_after();
         const uint32_t d = tmem + kTmS + (i & 1) * 64;
 #pragma unroll
         for (int s = 0; s < D / 16; ++s)
-          tc_mma_f16_words(d, k_lo + ((s >> 2) * 1024 + (s & 3) * 32) / 16, k_hi,
+          tc_mma_f16_words(d, k_lo + (SW ? (s >> 2) * 1024 + (s & 3) * 32 : s * 256) / 16, k_hi,
                            q_lo + ((s >> 2) * (N * 128) + (s & 3) * 32) / 16, q_hi, idesc_f16(N, 0, 0), s > 0 ? 1u : 0u);
         tc_commit(bar(kBarS0 + (i & 1)));
       };
@@ -1437,25 +1444,24 @@ SharedPlan make_plan(const Geometry& g, int batch, int n_groups, int max_group, 
   q.CH = 256;
   while ((max_own + q.CH - 1) / q.CH > 64) q.CH *= 2;
   q.NC = 1 + (max_own + q.CH - 1) / q.CH;                  // the window, and the chunks
-  // Both grids together fill the machine once, shared by their work (SM cycles,
-  // measured: a tile, a unit's setup, an own or window token).
-  const double t_tile = q.N > 32 ? 3300 : 2100, t_token = 13;
+  // Both grids together fill the machine once. The own grid gets the fewest blocks
+  // that end no later than the shared grid, by measured times (SM cycles): a tile;
+  // a block's 16 warps' way through a task each, which grows with its tokens.
+  const double t_tile = q.N == 16 ? 2200 : q.N == 32 ? 2700 : 3400;
   const int tiles = (max_shared + 4 * g.LB - 1) / (4 * g.LB);
-  const int64_t tiles_of_rows = n_groups * ((rows + q.N - 1) / q.N), by_batch = n_groups + static_cast<int64_t>(batch) * ratio / q.N;
-  const double units = max_shared > 0 ? static_cast<double>(tiles_of_rows < by_batch ? tiles_of_rows : by_batch) * g.Hkv : 0;
-  const double work_a = units * (tiles + 5) * t_tile;
-  const double work_b = static_cast<double>(batch) * g.Hq * (max_own * 0.75 + g.W) * t_token;
+  const int64_t of_rows = n_groups * ((rows + q.N - 1) / q.N), of_batch = n_groups + static_cast<int64_t>(batch) * ratio / q.N;
+  const double units = max_shared > 0 ? static_cast<double>(of_rows < of_batch ? of_rows : of_batch) * g.Hkv : 0;
   const int64_t tasks = static_cast<int64_t>(batch) * g.Hq * q.NC;
-  const int64_t most_b = (tasks + 15) / 16;
-  double nb = kPlanSms * work_b / (work_a + work_b) + 0.5;
-  // ... and the own grid's warps, each through its tasks one after the other (15
-  // thousand cycles of latency each), are done no later than the shared grid
-  const double lat = 1.25 * tasks / 16 * 15000 / (work_a / kPlanSms + 20000);
-  if (lat > nb) nb = lat;
-  if (nb < 1) nb = 1;
-  if (units > 0 && nb > kPlanSms / 2 && nb > kPlanSms * work_b / (work_a + work_b)) nb = kPlanSms * work_b / (work_a + work_b) + 1;
-  if (units > 0 && nb > kPlanSms - 1) nb = kPlanSms - 1;
-  q.own_blocks = static_cast<int>(nb < most_b ? nb : most_b);
+  const double t_task = 8000 + 125 * (g.W + 0.75 * max_own) / q.NC;
+  const int most_b = static_cast<int>(tasks < 16 * kPlanSms ? (tasks + 15) / 16 : kPlanSms);
+  int lo = 1, hi = units > 0 && most_b == kPlanSms ? kPlanSms - 1 : most_b;
+  while (lo < hi) {
+    const int nb = (lo + hi) / 2;
+    const double t_a = 8000 + units * (tiles + 5) * t_tile / (kPlanSms - nb);
+    const double t_b = static_cast<double>((tasks + 16 * nb - 1) / (16 * nb)) * t_task;
+    if (t_b <= t_a) hi = nb; else lo = nb + 1;
+  }
+  q.own_blocks = lo;
   if (units > 0) {
     const double most_a = units * tiles;
     const int na = kPlanSms - q.own_blocks;
