@@ -272,6 +272,9 @@ __device__ __forceinline__ float redux_fmax(float v) {
   return r;
 }
 
+// 2^k for -126 <= k <= 127.
+__device__ __forceinline__ float pow2(int k) { return __int_as_float((127 + k) << 23); }
+
 // Power of two that brings values of magnitude `top` just below 2^14 (1 for 0
 // or no finite value).
 __device__ __forceinline__ int scale_exp(float top) {
@@ -454,7 +457,7 @@ __global__ void __launch_bounds__(kE) shared_table_kernel(const float* cb_k, con
 #pragma unroll
     for (int i = 0; i < kE / 32; ++i) top = fmaxf(top, red[k][i]);
     const int ex = scale_exp(top);
-    const float f = ldexpf(1.f, ex);
+    const float f = pow2(ex);
     if (e == 0) exps[(h * 2 + kv) * 32 + j0 + k] = ex;
 #pragma unroll
     for (int i = 0; i < C / 4; ++i) {
@@ -529,7 +532,7 @@ __device__ __forceinline__ int64_t pair_of(const SharedParams& p, const Segment&
 template <int J, int C, int N>
 __device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const Segment& u, uint32_t tmem) {
   using T = Shape<J, C>;
-  constexpr int D = T::D, NC = N / 2;
+  constexpr int D = T::D, NC = N / 2, CW = NC < 16 ? NC : 16;
   // P: rows of 64 query rows and one buffer, or of 32 and two (the same bytes)
   constexpr int PP = N > 32 ? 128 : 64, PB = N > 32 ? 1 : 2;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -549,10 +552,7 @@ __device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const S
       asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar(i)), "r"(n) : "memory");
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    if (u.load) {
-      request_table(p, sm, hkv, 0, bar(kBarTabK));
-      request_table(p, sm, hkv, 1, bar(kBarTabV));
-    }
+    if (u.load) request_table(p, sm, hkv, 0, bar(kBarTabK));
   }
   const int* exk = p.exps + hkv * 64;
   // a row's shared tokens and its unset reference (the last threads; the first ones
@@ -576,7 +576,7 @@ __device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const S
       const uint32_t w[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float f2 = ldexpf(1.f, f < PIECES ? -__ldg(exk + (part * 8 + 2 * i) / C) : 0);
+        const float f2 = pow2(f < PIECES ? -__ldg(exk + (part * 8 + 2 * i) / C) : 0);
         const float2 a = bf16x2_to_float2(w[i]);
         v[k][2 * i] = a.x * f2;
         v[k][2 * i + 1] = a.y * f2;
@@ -584,7 +584,7 @@ __device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const S
       }
     }
     kq = scale_exp(block_max(top, red, tid));
-    const float f2 = ldexpf(1.f, kq);
+    const float f2 = pow2(kq);
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
       const int f = tid + k * kShThreads, c = f / (D / 8), byte = (f % (D / 8)) * 16;
@@ -666,7 +666,13 @@ __device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const S
     };
     uint32_t w0[W0], w1[W0];                               // tiles i and i + 1
     int nv0 = load_rows(0, w0), nv1 = load_rows(1, w1);
-    if (u.load) failed = !mbar_wait(bar(values ? kBarTabV : kBarTabK), 0, kShSpin);
+    if (u.load) {
+      // the value table follows the key table, so that the first keys need not
+      // share the way from L2 with it
+      failed = !mbar_wait(bar(kBarTabK), 0, kShSpin);
+      if (warp == kVWarp && lane == 0) request_table(p, sm, hkv, 1, bar(kBarTabV));
+      if (values) failed = !mbar_wait(bar(kBarTabV), 0, kShSpin) || failed;
+    }
 #pragma unroll 1
     for (int i = 0; i < nt; ++i) {
       // the tile is free when S^T (K) or O^T (V) of the tile before is done
@@ -753,27 +759,36 @@ __device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const S
       failed = !mbar_wait(bar(kBarS0 + (i & 1)), (i >> 1) & 1, kShSpin);
       __syncwarp();
       tc_after();
-      uint32_t sv[NC];
-      tld<NC>(lanes + kTmS + (i & 1) * 64 + c0, sv);
       const int nv = nvs[(i & 3) * 4 + quad];
-      tld_wait();
-      if (nv < 32 && lane >= nv) {                         // no token in this slot
+      const bool masked = tok0 + (i + 1) * T::TOK > min_lim;   // some row ends inside this tile
+      const int tok = tok0 + i * T::TOK + quad * T::LB + lane;
+      // CW columns of this token's scores, -inf where there is none (read again for
+      // each use when the half has more than CW: registers)
+      auto scores = [&](int c, uint32_t (&sv)[CW]) {
+        tld<CW>(lanes + kTmS + (i & 1) * 64 + c0 + c, sv);
+        tld_wait();
+        if (nv < 32 && lane >= nv) {                       // no token in this slot
 #pragma unroll
-        for (int c = 0; c < NC; ++c) sv[c] = 0xff800000u;  // -inf
-      }
-      if (tok0 + (i + 1) * T::TOK > min_lim) {             // some row ends inside this tile
-        const int tok = tok0 + i * T::TOK + quad * T::LB + lane;
+          for (int k = 0; k < CW; ++k) sv[k] = 0xff800000u;
+        }
+        if (masked) {
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
-          if (tok >= lim[c0 + c]) sv[c] = 0xff800000u;
-      }
+          for (int k = 0; k < CW; ++k)
+            if (tok >= lim[c0 + c + k]) sv[k] = 0xff800000u;
+        }
+      };
+      uint32_t sv[CW];
       float mx = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < NC; c += 4) {
-        const float4 mm = m4[c / 4];
-        mx = fmaxf(mx, fmaxf(fmaf(__uint_as_float(sv[c]), scale, -mm.x), fmaf(__uint_as_float(sv[c + 1]), scale, -mm.y)));
-        mx = fmaxf(mx, fmaxf(fmaf(__uint_as_float(sv[c + 2]), scale, -mm.z),
-                             fmaf(__uint_as_float(sv[c + 3]), scale, -mm.w)));
+      for (int c = 0; c < NC; c += CW) {
+        scores(c, sv);
+#pragma unroll
+        for (int k = 0; k < CW; k += 4) {
+          const float4 mm = m4[(c + k) / 4];
+          mx = fmaxf(mx, fmaxf(fmaf(__uint_as_float(sv[k]), scale, -mm.x), fmaf(__uint_as_float(sv[k + 1]), scale, -mm.y)));
+          mx = fmaxf(mx, fmaxf(fmaf(__uint_as_float(sv[k + 2]), scale, -mm.z),
+                               fmaf(__uint_as_float(sv[k + 3]), scale, -mm.w)));
+        }
       }
       if (i >= PB) failed = !mbar_wait(bar(kBarO0 + ((i - PB) & 1)), ((i - PB) >> 1) & 1, kShSpin) || failed;
       if (named_or(bar_id, 128, mx > kRaise || failed)) {
@@ -788,9 +803,13 @@ __device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const S
         // keeps column c's maximum over the warp's tokens.
         float top = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          const float t = redux_fmax(__uint_as_float(sv[c]) * scale);
-          if (lane == c) top = t;
+        for (int c = 0; c < NC; c += CW) {
+          if (NC > CW) scores(c, sv);
+#pragma unroll
+          for (int k = 0; k < CW; ++k) {
+            const float t = redux_fmax(__uint_as_float(sv[k]) * scale);
+            if (lane == c + k) top = t;
+          }
         }
         if (lane < NC) cm[quad * kMaxRows + c0 + lane] = top;
         named_sync(bar_id, 128);
@@ -828,23 +847,27 @@ __device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const S
       unsigned char* prow = sm + kPOff + (i % PB) * (kTileRows * PP) + row * PP;
       const int swz = PP == 128 ? row & 7 : (row >> 1) & 3;
 #pragma unroll
-      for (int c = 0; c < NC; c += 8) {
-        uint32_t w[4];
+      for (int cc = 0; cc < NC; cc += CW) {
+        if (NC > CW) scores(cc, sv);
 #pragma unroll
-        for (int k = 0; k < 4; k += 2) {
-          const float4 mm = m4[(c + 2 * k) / 4];
-          const float e0 = fast_exp2(fmaf(__uint_as_float(sv[c + 2 * k]), scale, -mm.x));
-          const float e1 = fast_exp2(fmaf(__uint_as_float(sv[c + 2 * k + 1]), scale, -mm.y));
-          const float e2 = fast_exp2(fmaf(__uint_as_float(sv[c + 2 * k + 2]), scale, -mm.z));
-          const float e3 = fast_exp2(fmaf(__uint_as_float(sv[c + 2 * k + 3]), scale, -mm.w));
-          l[c + 2 * k] += e0;
-          l[c + 2 * k + 1] += e1;
-          l[c + 2 * k + 2] += e2;
-          l[c + 2 * k + 3] += e3;
-          w[k] = half2_bits(e0, e1);
-          w[k + 1] = half2_bits(e2, e3);
+        for (int c = 0; c < CW; c += 8) {
+          uint32_t w[4];
+#pragma unroll
+          for (int k = 0; k < 4; k += 2) {
+            const float4 mm = m4[(cc + c + 2 * k) / 4];
+            const float e0 = fast_exp2(fmaf(__uint_as_float(sv[c + 2 * k]), scale, -mm.x));
+            const float e1 = fast_exp2(fmaf(__uint_as_float(sv[c + 2 * k + 1]), scale, -mm.y));
+            const float e2 = fast_exp2(fmaf(__uint_as_float(sv[c + 2 * k + 2]), scale, -mm.z));
+            const float e3 = fast_exp2(fmaf(__uint_as_float(sv[c + 2 * k + 3]), scale, -mm.w));
+            l[cc + c + 2 * k] += e0;
+            l[cc + c + 2 * k + 1] += e1;
+            l[cc + c + 2 * k + 2] += e2;
+            l[cc + c + 2 * k + 3] += e3;
+            w[k] = half2_bits(e0, e1);
+            w[k + 1] = half2_bits(e2, e3);
+          }
+          *reinterpret_cast<uint4*>(prow + ((((c0 + cc + c) >> 3) ^ swz) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        *reinterpret_cast<uint4*>(prow + ((((c0 + c) >> 3) ^ swz) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
       }
       proxy_fence();
       tc_before();
@@ -857,7 +880,7 @@ __device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const S
     if (!failed) {
       // ---- the rows' records: o from TMEM (lane = channel), m and l ------------------
       tc_after();
-      const float unscale = row < D ? ldexpf(1.f, -__ldg(exk + 32 + row / C)) : 0.f;
+      const float unscale = row < D ? pow2(-__ldg(exk + 32 + row / C)) : 0.f;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         const float t = warp_sum(l[c]);
@@ -1313,7 +1336,7 @@ __global__ void __launch_bounds__(kOwnWarps * 32, 1) shared_own_kernel(const Sha
    if (!failed) {
     __syncthreads();                                       // the head before is done with tables and scales
     if (tid < 2) request_table(p, sm, hkv, tid, bar);
-    if (tid < J) fk[tid] = ldexpf(1.f, -__ldg(exk + tid));
+    if (tid < J) fk[tid] = pow2(-__ldg(exk + tid));
     failed = __syncthreads_or(!mbar_wait(bar, phase & 1, kShSpin));
     if (failed && tid == 0) {                              // no copy may outlive the block
       const bool drained = mbar_wait(bar, phase & 1, kShDrainSpin);
@@ -1322,7 +1345,7 @@ __global__ void __launch_bounds__(kOwnWarps * 32, 1) shared_own_kernel(const Sha
                                    : (LOOPVQ_DECODE_STATUS_TIMEOUT | LOOPVQ_DECODE_STATUS_UNDRAINED));
     }
    }
-   const float unv = lane < J ? ldexpf(1.f, -__ldg(exk + 32 + lane)) : 0.f;   // of this lane's record channels
+   const float unv = lane < J ? pow2(-__ldg(exk + 32 + lane)) : 0.f;   // of this lane's record channels
    const uint8_t* pool_h = p.pool_lg + hkv * p.pool_stride_head;
    for (int ti = th + warp; ti < t_end; ti += kOwnWarps) {
     const int t = ti - hkv * per_head;
@@ -1361,7 +1384,7 @@ __global__ void __launch_bounds__(kOwnWarps * 32, 1) shared_own_kernel(const Sha
       top = fmaxf(top, fmaxf(finite_abs(f[k].x), finite_abs(f[k].y)));
     }
     const int kq = scale_exp(redux_fmax(top));
-    const float fq = ldexpf(1.f, kq);
+    const float fq = pow2(kq);
     __syncwarp();
 #pragma unroll
     for (int k = 0; k < PER; ++k)
