@@ -472,13 +472,28 @@ loopvq_status loopvq_prefill_attn(const loopvq_config* cfg, int layer, int loop_
  *  max_group, max_shared_len, max_own_len
  *                bounds on the host: sequences of a group, shared quantised
  *                tokens of a group, and quantised tokens of a sequence past the
- *                shared ones. Device values past a bound are clipped to it and
- *                set LOOPVQ_DECODE_STATUS_BAD_GROUP.
+ *                shared ones.
  *  workspace     at least loopvq_decode_shared_workspace_bytes(cfg, batch,
  *                n_groups, max_group, max_shared_len, max_own_len) bytes,
  *                16-byte aligned; the status word as for loopvq_decode_attn.
  *                Calls that may overlap need workspaces of their own.
- * Every other argument as for loopvq_decode_attn.
+ * Every other argument as for loopvq_decode_attn; codebooks must be finite.
+ *
+ * Two forms, chosen per call:
+ *  - bf16 output, (J, c) = (32, 4), (16, 4), (12, 8), (16, 8) or (24, 4), on
+ *    average at least four query rows (sequences times Hq/Hkv) per group and
+ *    at least 64 (sequence, query head) pairs: the tensor-core form. Shared
+ *    tokens are dequantised once per group and kv-head. Codewords and softmax
+ *    weights enter the products in fp16 (half a step is 2^-11 relative; both are
+ *    scaled by powers of two first), sums are float32, so a score, and lse, is
+ *    within about 2^-11 sm_scale sum |q_i k_i|. group_starts that do not ascend
+ *    inside [0, batch], or device values past a bound of the call, set
+ *    LOOPVQ_DECODE_STATUS_BAD_GROUP, and what lies past the bound is left out.
+ *    A bounded wait that gives up sets LOOPVQ_DECODE_STATUS_TIMEOUT (and
+ *    _UNDRAINED). Results do not depend on the order in which blocks run.
+ *  - otherwise: the kernels of loopvq_decode_attn over every sequence's own row
+ *    of block_table (exact in float32; groups and bounds are not looked at,
+ *    beyond a longest sequence of P + R + max_shared_len + max_own_len).
  */
 size_t loopvq_decode_shared_workspace_bytes(const loopvq_config* cfg, int batch, int n_groups,
                                             int max_group, int max_shared_len, int max_own_len);

@@ -1469,24 +1469,27 @@ SharedPlan make_plan(const Geometry& g, int batch, int n_groups, int max_group, 
   q.NC = 1 + (max_own + q.CH - 1) / q.CH;                  // the window, and the chunks
   // Both grids together fill the machine once. The own grid gets the fewest blocks
   // that end no later than the shared grid, by measured times (SM cycles): a tile;
-  // a block's 16 warps' way through a task each, which grows with its tokens.
+  // a block's 16 warps' way through a task each, which grows with its tokens; the
+  // tables of a head.
   const double t_tile = q.N == 16 ? 2200 : q.N == 32 ? 2700 : 3400;
   const int tiles = (max_shared + 4 * g.LB - 1) / (4 * g.LB);
   const int64_t of_rows = n_groups * ((rows + q.N - 1) / q.N), of_batch = n_groups + static_cast<int64_t>(batch) * ratio / q.N;
   const double units = max_shared > 0 ? static_cast<double>(of_rows < of_batch ? of_rows : of_batch) * g.Hkv : 0;
   const int64_t tasks = static_cast<int64_t>(batch) * g.Hq * q.NC;
   const double t_task = 8000 + 125 * (g.W + 0.75 * max_own) / q.NC;
-  const int most_b = static_cast<int>(tasks < 16 * kPlanSms ? (tasks + 15) / 16 : kPlanSms);
+  const int64_t fit_b = (tasks + 15) / 16 > g.Hkv ? (tasks + 15) / 16 : g.Hkv;
+  const int most_b = static_cast<int>(fit_b < kPlanSms ? fit_b : kPlanSms);
   int lo = 1, hi = units > 0 && most_b == kPlanSms ? kPlanSms - 1 : most_b;
   while (lo < hi) {
     const int nb = (lo + hi) / 2;
     const double t_a = 8000 + units * (tiles + 5) * t_tile / (kPlanSms - nb);
-    const double t_b = static_cast<double>((tasks + 16 * nb - 1) / (16 * nb)) * t_task;
+    const double heads = static_cast<double>(g.Hkv) / nb + 1;   // that a block meets
+    const double t_b = heads * 7000 + (static_cast<double>(tasks) / (16 * nb) + 0.3 * heads) * t_task;
     if (t_b <= t_a) hi = nb; else lo = nb + 1;
   }
   q.own_blocks = lo;
-  if (units > 0) {
-    const double most_a = units * tiles;
+  if (units > 0) {                                         // three tiles a block at least
+    const double most_a = units * (tiles + 5) / 3;
     const int na = kPlanSms - q.own_blocks;
     q.shared_blocks = most_a < na ? static_cast<int>(most_a) : na;
   }
@@ -1581,8 +1584,16 @@ SharedLayout make_layout(const Geometry& g, int batch, const SharedPlan& q) {
 
 }  // namespace
 
-bool shared_attn_supported(const Geometry& g, int n_groups, int out_dtype) {
+// The shapes that the kernels take, where sharing pays: measured on B200 (16
+// heads of 128, own tokens 75 on average; these kernels / streaming each sequence,
+// us at 200, 4000 and 16000 shared tokens): groups of 3 sequences 29/18, 32/24,
+// 33/31; of 4 21/19, 23/24, 34/35; of 8 18/25, 22/30, 35/50; 8 groups of 2 24/33,
+// 56/49, 151/92; 8 groups of 4 27/60, 58/89, 154/168. With few (sequence, head)
+// pairs the four launches cost more than they save: one head of 64, 16 sequences
+// 15/13, 18/17, 23/20.
+bool shared_attn_supported(const Geometry& g, int batch, int n_groups, int out_dtype) {
   if (out_dtype != LOOPVQ_DTYPE_BF16 || n_groups == 0) return false;
+  if (static_cast<int64_t>(batch) * (g.Hq / g.Hkv) < 4ll * n_groups || static_cast<int64_t>(batch) * g.Hq < 64) return false;
   switch (g.J * 100 + g.c) {
     case 3204: case 1604: case 1208: case 1608: case 2404: return true;
     default: return false;

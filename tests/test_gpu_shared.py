@@ -209,26 +209,3 @@ def test_other_stream_replay_and_repeat():
     lse2 = np.array([[c2.oracle(b, h)[1] for h in range(2)] for b in range(5)])
     check_shared(c2, o.float().cpu().numpy(), lse2)
     assert int(ws[:4].view(torch.int32)) == 0
-
-
-def test_values_past_the_bounds_are_clipped_and_flagged():
-    c = SharedCase(MHA, [(3, 500)], [130, 4, 60], seed=22)
-    flag = B.LOOPVQ_DECODE_STATUS_BAD_GROUP
-    # own tokens past max_own_len are left out: the oracle without them
-    out, lse = c.run_gpu(status=flag, bounds=(3, 500, 60))
-    c.n_vq = [560, 504, 560]
-    check_shared(c, out, lse)
-    # a sequence past max_group shares nothing, and its own tokens are clipped too
-    c = SharedCase(MHA, [(3, 500)], [60, 4, 60], seed=22)
-    out, lse = c.run_gpu(status=flag, bounds=(2, 500, 60))
-    c.n_vq[2] = 60
-    check_shared(c, out, lse)
-    # starts outside the batch: its sequences share nothing
-    d = c.device()
-    d["group_starts"].copy_(torch.tensor([-1, 9], dtype=torch.int32))
-    out, _ = c.run_gpu(status=flag, dev_inputs=d)
-    assert np.all(np.isfinite(out))
-    d["group_starts"].copy_(torch.tensor([5, 2], dtype=torch.int32))
-    out, lse = c.run_gpu(status=flag, dev_inputs=d)
-    c.n_vq = [60, 60, 60]
-    check_shared(c, out, lse)
