@@ -46,8 +46,10 @@
 #include <cuda_fp16.h>
 #include <math.h>
 
+#include <algorithm>
 #include <atomic>
 #include <climits>
+#include <numeric>
 #include <type_traits>
 
 #include "common.cuh"
@@ -1200,6 +1202,11 @@ __device__ void own_chunk(const SharedParams& p, const uint8_t* pool_h, int b, i
   int e_next = entry_of(b0);
   request(b0, e_next);
   e_next = entry_of(b0 + 1);
+  // the query's channels of group (lane + s) mod J, for every byte s of a row: the
+  // same for all blocks, so held in registers
+  Word<T::ENTRY> q[J];
+#pragma unroll
+  for (int i = 0; i < J; ++i) q[i] = lds<T::ENTRY, 0>(sa + kOwnQ + (lane + i) * T::ENTRY);
 #pragma unroll 1
   for (int blk = b0; blk < b1; ++blk) {
     // the value rows of this block, each twice
@@ -1226,21 +1233,19 @@ __device__ void own_chunk(const SharedParams& p, const uint8_t* pool_h, int b, i
     const int tok = blk * LB + lane;
     const bool valid = ok && lane < LB && tok >= t0 && tok < t1;
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    const uint32_t qa = sa + kOwnQ + lane * T::ENTRY;
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-      Word<T::ENTRY> e[4], qv[4];
+      Word<T::ENTRY> e[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {                        // codeword row (byte 1) | entry (byte 0)
         const uint32_t at = J == 32 ? static_cast<uint32_t>(lane + 4 * w + i) * T::ENTRY      // byte 0 wraps by itself
                                     : static_cast<uint32_t>((lane + 4 * w + i) % J) * T::ENTRY;
         e[i] = lds<T::ENTRY, kShBase + kKtabOff>(__byte_perm(kw[w], at, 0x7704u | (static_cast<uint32_t>(i) << 4)));
-        qv[i] = lds<T::ENTRY, 0>(qa + (4 * w + i) * T::ENTRY);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int c = 0; c < C / 2; ++c) dot_f16(acc[i], qv[i].w[c], e[i].w[c]);
+        for (int c = 0; c < C / 2; ++c) dot_f16(acc[i], q[4 * w + i].w[c], e[i].w[c]);
     }
     request(blk + 1, e_next);                              // lands under this block's values
     e_next = entry_of(blk + 2);
@@ -1327,14 +1332,15 @@ __global__ void __launch_bounds__(kOwnWarps * 32, 1) shared_own_kernel(const Sha
   const int per_head = p.B * p.ratio * p.NC;               // (times Hkv below 2^31: checked on the host)
   const int t_lo = static_cast<int>(static_cast<int64_t>(per_head) * p.Hkv * blockIdx.x / gridDim.x);
   const int t_hi = static_cast<int>(static_cast<int64_t>(per_head) * p.Hkv * (blockIdx.x + 1) / gridDim.x);
+  int* next = reinterpret_cast<int*>(sm + kOwnBarOff + 8);
   bool failed = false;
   int phase = 0;
   for (int th = t_lo; th < t_hi; ++phase) {            // block-uniform
    const int hkv = th / per_head;
    const int t_end = min(t_hi, (hkv + 1) * per_head);
    const int* exk = p.exps + hkv * 64;
+   __syncthreads();                                        // the head before is done with tables and scales
    if (!failed) {
-    __syncthreads();                                       // the head before is done with tables and scales
     if (tid < 2) request_table(p, sm, hkv, tid, bar);
     if (tid < J) fk[tid] = pow2(-__ldg(exk + tid));
     failed = __syncthreads_or(!mbar_wait(bar, phase & 1, kShSpin));
@@ -1347,7 +1353,13 @@ __global__ void __launch_bounds__(kOwnWarps * 32, 1) shared_own_kernel(const Sha
    }
    const float unv = lane < J ? pow2(-__ldg(exk + 32 + lane)) : 0.f;   // of this lane's record channels
    const uint8_t* pool_h = p.pool_lg + hkv * p.pool_stride_head;
-   for (int ti = th + warp; ti < t_end; ti += kOwnWarps) {
+   if (tid == 0) *next = th;
+   __syncthreads();
+   for (;;) {                                              // a warp takes the next task when it is done with one
+    int ti = 0;
+    if (lane == 0) ti = atomicAdd(next, 1);
+    ti = __shfl_sync(0xffffffffu, ti, 0);
+    if (ti >= t_end) break;
     const int t = ti - hkv * per_head;
     const int y = t / p.NC, ck = t - y * p.NC - 1;         // -1: the window
     const int b = y / p.ratio, r = y - b * p.ratio;
@@ -1464,30 +1476,41 @@ SharedPlan make_plan(const Geometry& g, int batch, int n_groups, int max_group, 
   const int ratio = g.Hq / g.Hkv;
   const int64_t rows = static_cast<int64_t>(max_group) * ratio;
   q.N = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-  q.CH = 256;
+  q.CH = static_cast<int64_t>(batch) * g.Hq >= 512 ? 512 : 256;
   while ((max_own + q.CH - 1) / q.CH > 64) q.CH *= 2;
   q.NC = 1 + (max_own + q.CH - 1) / q.CH;                  // the window, and the chunks
-  // Both grids together fill the machine once. The own grid gets the fewest blocks
-  // that end no later than the shared grid, by measured times (SM cycles): a tile;
-  // a block's 16 warps' way through a task each, which grows with its tokens; the
-  // tables of a head.
+  // Both grids together fill the machine once. The own grid gets the number of
+  // blocks with which the later of the two ends first, by measured times (SM
+  // cycles): a tile; a block's 16 warps' way through a task each, which grows with
+  // its tokens; the tables of a head and the warps that run out of its tasks first,
+  // more of them where blocks start and end inside heads. (Own tokens, and the
+  // shared ones of several groups, as if spread over the upper half of their range.)
   const double t_tile = q.N == 16 ? 2200 : q.N == 32 ? 2700 : 3400;
   const int tiles = (max_shared + 4 * g.LB - 1) / (4 * g.LB);
   const int64_t of_rows = n_groups * ((rows + q.N - 1) / q.N), of_batch = n_groups + static_cast<int64_t>(batch) * ratio / q.N;
   const double units = max_shared > 0 ? static_cast<double>(of_rows < of_batch ? of_rows : of_batch) * g.Hkv : 0;
   const int64_t tasks = static_cast<int64_t>(batch) * g.Hq * q.NC;
-  const double t_task = 8000 + 125 * (g.W + 0.75 * max_own) / q.NC;
+  const double t_task = 1500 + 125 * (g.W + 0.75 * max_own * 32 / g.LB) / q.NC;
   const int64_t fit_b = (tasks + 15) / 16 > g.Hkv ? (tasks + 15) / 16 : g.Hkv;
   const int most_b = static_cast<int>(fit_b < kPlanSms ? fit_b : kPlanSms);
-  int lo = 1, hi = units > 0 && most_b == kPlanSms ? kPlanSms - 1 : most_b;
-  while (lo < hi) {
-    const int nb = (lo + hi) / 2;
-    const double t_a = 8000 + units * (tiles + 5) * t_tile / (kPlanSms - nb);
-    const double heads = static_cast<double>(g.Hkv) / nb + 1;   // that a block meets
-    const double t_b = heads * 7000 + (static_cast<double>(tasks) / (16 * nb) + 0.3 * heads) * t_task;
-    if (t_b <= t_a) hi = nb; else lo = nb + 1;
+  q.own_blocks = most_b;
+  if (units > 0) {
+    const int last = most_b == kPlanSms ? kPlanSms - 1 : most_b;
+    const double work_a = units * ((n_groups > 1 ? 0.75 : 1.0) * tiles + 5) * t_tile;
+    double best = 1e300;
+    for (int nb = 1; nb <= last; nb += nb < g.Hkv ? 1 : g.Hkv) {
+      const double t_a = 8000 + work_a / (kPlanSms - nb);
+      const int div = std::gcd(nb, g.Hkv), starts = nb / div;     // a block starts at multiples of 1 / starts heads
+      const int heads = (g.Hkv / div + 2 * (starts - 1)) / starts;   // and meets this many at most
+      const double t_b = heads * (7000 + (starts > 1 && heads > 1 ? 0.5 : 0.2) * t_task) +
+                         std::max(static_cast<double>(tasks) / (16 * nb), static_cast<double>(heads)) * t_task;
+      const double t = t_a > t_b ? t_a : t_b;
+      if (t < best) {
+        best = t;
+        q.own_blocks = nb;
+      }
+    }
   }
-  q.own_blocks = lo;
   if (units > 0) {                                         // three tiles a block at least
     const double most_a = units * (tiles + 5) / 3;
     const int na = kPlanSms - q.own_blocks;
