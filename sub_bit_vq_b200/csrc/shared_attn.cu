@@ -9,29 +9,32 @@
 // The tokens (then the channels) are the M side, so the products cost what the
 // group's rows need (N = 16, 32 or 64) and not a 128-row tile.
 //
-// Three parts of one grid and one merge:
-//   shared blocks  (group, kv-head, row tile, split of the shared tokens): the
-//                  tensor-core pipeline below, one record (m, l, o[d]) per row.
-//   own blocks     (kv-head, part): one warp per (sequence, query head, chunk
-//                  of its own quantised tokens), scored against the same
-//                  codebooks in shared memory, lane = channel group; chunk 0
-//                  takes the bf16 window too. One record per chunk.
-//   merge kernel   log-sum-exp join of a pair's records.
+// Four kernels, each a programmatic dependent of the one before:
+//   shared_table_kernel   the call's codebook slices as fp16 tables, every
+//                  sequence's split into shared and own tokens, the shared grid's
+//                  starting points. 128 KB a head.
+//   shared_prefix_kernel  persistent blocks over the tiles of all units (group, row
+//                  tile, head): the tensor-core pipeline below, one record
+//                  (m, l, o[d]) per row and block that met it.
+//   shared_own_kernel     beside it, on the SMs that it leaves free: a warp per
+//                  (sequence, query head, window or chunk of own quantised
+//                  tokens), scored against the same tables without a product.
+//   shared_merge_kernel   log-sum-exp join of a row's records.
 //
 // Codewords are dequantised from fp16 tables in shared memory, [E] rows of 256
 // bytes holding entry (e, j) at byte j*2c: a lane that reads channel group j
 // hits banks that depend on j only, and in the pool's rotated rows lane = slot i
 // finds group (s + i) mod J at byte s, so the lookups of a half-warp never
-// collide. The tile rows are written in the 128-byte swizzle, where the same
-// rotation keeps the stores free of conflicts too. The value tile is the same
-// [token][channel] layout read as an M-major operand, so nothing is transposed.
+// collide. The tile rows are written so that the same rotation keeps the stores
+// free of conflicts too (tile_off). The value tile is the same [token][channel]
+// layout read as an M-major operand, so nothing is transposed.
 //
-// Shared pipeline, 17 warps: warps 8-15 dequantise (a tile is four index
-// blocks; warp w fills block w % 4, half of its groups), warp 16 issues the
-// products, warps 0-7 turn S^T into P (warp w reads TMEM lanes 32 (w % 4) ..,
-// the column half w / 4). K has one buffer, V one per half tile, S^T two, P one;
-// mbarriers hand them over, so the dequantisation of tile i + 1 runs under the
-// softmax of tile i.
+// Shared pipeline, 25 warps: 0-7 turn S^T into P (warp w reads TMEM lanes
+// 32 (w % 4) .., the column half w / 4), 8-15 fill the K tile and 16-23 the V tile
+// (a tile is four index blocks; warp w fills block w % 4, half of its groups), 24
+// issues the products. K and V have one buffer each, S^T two, P two (one with 64
+// rows); mbarriers hand them over, so the next K tile is filled under the softmax
+// and the next V tile under the next scores.
 //
 // Softmax: per row a reference m, raised only when a score passes it by more
 // than kRaise (then to the tile's maximum - kTop), so P = 2^(x - m) stays below
@@ -42,6 +45,22 @@
 // 2^-11 of each value, an eighth of the bf16 output's own. Codebooks and queries
 // are scaled by powers of two into fp16's range (exact), so their magnitude does
 // not matter. float32 outputs take the streaming kernels.
+//
+// Cost. HBM has to deliver a group's indices once (8 sequences of 16 heads over
+// 32696 tokens: 33.5 MB, 5 us); the products are small. What a tile costs is
+// shared-memory accesses: 2 x 32 KB of lookups, as much of stores, and the
+// products' reads, 1650 cycles of 128 bytes with 16 query rows, 1900 with 64.
+// Measured 2200 and 3400 (1900 MHz): 52.5 us for those 8 sequences, of which 47 in
+// the shared grid (7 of them before its first tile), 5 + 1 around it in the tables
+// and the merge, against 77.9 us when every sequence streams on its own; 256
+// sequences over 16312 tokens 200 us against 1313.
+//
+// What lost: the keys in two half tiles of M = 64 (71 us for the 8 sequences: a
+// product takes 90-150 cycles of issue under the fill's accesses, 47 alone, so
+// more and smaller ones lose); values handed over block by block (73: polls queue
+// behind the fill's accesses); one team filling both planes (61); products issued
+// by a warp of each fill team instead of one of their own, with 16 softmax warps at
+// 64 rows (61, and 233 for the 256 sequences).
 
 #include <cuda_fp16.h>
 #include <math.h>
@@ -406,7 +425,9 @@ __device__ void plan_walks(const SharedParams& p) {
 // The codebook slices of one call as fp16 tables: block (4 channel groups, K or
 // V, head), thread = codeword. Each group is scaled by a power of two of its
 // own. Also the split of every sequence into shared and own tokens and, in a block
-// of its own, where the shared grid's blocks start. Blocks of the attention grid start meanwhile and wait for this grid.
+// of its own, where the shared grid's blocks start. The shared grid's blocks start
+// meanwhile and wait for this grid. 16 heads of 128 read 4.2 MB and write 2.1 MB in
+// 5.4 us, a launch's latency and two dependent loads.
 template <int J, int C, int N>
 __global__ void __launch_bounds__(kE) shared_table_kernel(const float* cb_k, const float* cb_v, int64_t cb_stride_head,
                                                           unsigned char* tables, int* exps, const SharedParams p) {
@@ -933,6 +954,11 @@ __device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const S
 // every block does the same work whatever the groups' sizes and lengths, and
 // meets one or a few units. Its records go to rows R + c*N .., R the rows of the
 // units before: since R and c both grow along the blocks, no two collide.
+// 16 x 32696 tokens of d = 128 with 8 rows on 140 blocks: 47.5 us, 36 MB from HBM
+// (0.75 TB/s: not the bound), shared-memory lookups and stores at 44% of an SM's
+// rate and the products' reads at 26% by their bytes; the rest is the hand-over
+// between fill, products and softmax. With 64 rows on 100 blocks, 16312 tokens of
+// 16 heads and 4 row tiles: 162 us.
 template <int J, int C, int N>
 __global__ void __launch_bounds__(kShThreads, 1) shared_prefix_kernel(const SharedParams p) {
   using T = Shape<J, C>;
@@ -1306,7 +1332,11 @@ __device__ void own_chunk(const SharedParams& p, const uint8_t* pool_h, int b, i
 }
 
 // Runs beside the shared grid, on the SMs that it leaves free: the shared blocks
-// start this grid once the tables are written.
+// start this grid once the tables are written. Without a group's worth of rows
+// there is no product to make; the bound is shared memory again, 6 accesses of 128
+// bytes a token (two for the keys' lookups, two for the values', two for indices
+// and weights): alone on 140 SMs with 1.5 M (sequence, head, token) triples and
+// 4096 windows 77.7 us, l1tex at 75%, 62% of the issue slots.
 template <int J, int C>
 __global__ void __launch_bounds__(kOwnWarps * 32, 1) shared_own_kernel(const SharedParams p) {
   using T = Shape<J, C>;
@@ -1335,82 +1365,84 @@ __global__ void __launch_bounds__(kOwnWarps * 32, 1) shared_own_kernel(const Sha
   int* next = reinterpret_cast<int*>(sm + kOwnBarOff + 8);
   bool failed = false;
   int phase = 0;
-  for (int th = t_lo; th < t_hi; ++phase) {            // block-uniform
-   const int hkv = th / per_head;
-   const int t_end = min(t_hi, (hkv + 1) * per_head);
-   const int* exk = p.exps + hkv * 64;
-   __syncthreads();                                        // the head before is done with tables and scales
-   if (!failed) {
-    if (tid < 2) request_table(p, sm, hkv, tid, bar);
-    if (tid < J) fk[tid] = pow2(-__ldg(exk + tid));
-    failed = __syncthreads_or(!mbar_wait(bar, phase & 1, kShSpin));
-    if (failed && tid == 0) {                              // no copy may outlive the block
-      const bool drained = mbar_wait(bar, phase & 1, kShDrainSpin);
-      if (p.status != nullptr)
-        atomicOr(p.status, drained ? LOOPVQ_DECODE_STATUS_TIMEOUT
-                                   : (LOOPVQ_DECODE_STATUS_TIMEOUT | LOOPVQ_DECODE_STATUS_UNDRAINED));
-    }
-   }
-   const float unv = lane < J ? pow2(-__ldg(exk + 32 + lane)) : 0.f;   // of this lane's record channels
-   const uint8_t* pool_h = p.pool_lg + hkv * p.pool_stride_head;
-   if (tid == 0) *next = th;
-   __syncthreads();
-   for (;;) {                                              // a warp takes the next task when it is done with one
-    int ti = 0;
-    if (lane == 0) ti = atomicAdd(next, 1);
-    ti = __shfl_sync(0xffffffffu, ti, 0);
-    if (ti >= t_end) break;
-    const int t = ti - hkv * per_head;
-    const int y = t / p.NC, ck = t - y * p.NC - 1;         // -1: the window
-    const int b = y / p.ratio, r = y - b * p.ratio;
-    const int64_t pair = static_cast<int64_t>(b) * p.Hq + hkv * p.ratio + r;
-    float* rec = p.orec + (pair * p.NC + ck + 1) * T::RS;
-    if (failed) {
-      if (lane == 0) {
-        rec[0] = NAN;
-        rec[1] = 1.f;
+  for (int th = t_lo; th < t_hi; ++phase) {                // block-uniform
+    const int hkv = th / per_head;
+    const int t_end = min(t_hi, (hkv + 1) * per_head);
+    const int* exk = p.exps + hkv * 64;
+    __syncthreads();                                       // the head before is done with tables and scales
+    if (!failed) {
+      if (tid < 2) request_table(p, sm, hkv, tid, bar);
+      if (tid < J) fk[tid] = pow2(-__ldg(exk + tid));
+      failed = __syncthreads_or(!mbar_wait(bar, phase & 1, kShSpin));
+      if (failed && tid == 0) {                            // no copy may outlive the block
+        const bool drained = mbar_wait(bar, phase & 1, kShDrainSpin);
+        if (p.status != nullptr)
+          atomicOr(p.status, drained ? LOOPVQ_DECODE_STATUS_TIMEOUT
+                                     : (LOOPVQ_DECODE_STATUS_TIMEOUT | LOOPVQ_DECODE_STATUS_UNDRAINED));
       }
-      continue;
     }
-    if (ck < 0) {
-      own_window<D>(p, static_cast<int64_t>(b) * p.Hkv + hkv, max(0, min(__ldg(p.seq_lens + b), p.W)), p.q + pair * D, rec, lane);
-      continue;
-    }
-    const int2 seq = __ldg(p.seqs + b);                    // its shared tokens, its own
-    const int t0 = seq.x + ck * p.CH, t1 = min(seq.x + seq.y, t0 + p.CH);
-    if (t0 >= t1) continue;                                // the merge does not read it
-    // the query in fp16 against the scales of the key groups: word i holds
-    // channels 2i, 2i + 1 (of D, then around again)
-    static_assert((31 + J) * C * 2 <= kOwnP - kOwnQ, "query entries 0 .. 30 + J fit");
-    const uint32_t* qw = reinterpret_cast<const uint32_t*>(p.q + pair * D);
-    constexpr int QW = (31 + J) * C / 2, PER = (QW + 31) / 32;
-    float2 f[PER];
-    float top = 0.f;
+    const float unv = lane < J ? pow2(-__ldg(exk + 32 + lane)) : 0.f;  // of this lane's record channels
+    const uint8_t* pool_h = p.pool_lg + hkv * p.pool_stride_head;
+    if (tid == 0) *next = th;
+    __syncthreads();
+    for (;;) {                                             // a warp takes the next task when it is done with one
+      int ti = 0;
+      if (lane == 0) ti = atomicAdd(next, 1);
+      ti = __shfl_sync(0xffffffffu, ti, 0);
+      if (ti >= t_end) break;
+      const int t = ti - hkv * per_head;
+      const int y = t / p.NC, ck = t - y * p.NC - 1;       // -1: the window
+      const int b = y / p.ratio, r = y - b * p.ratio;
+      const int64_t pair = static_cast<int64_t>(b) * p.Hq + hkv * p.ratio + r;
+      float* rec = p.orec + (pair * p.NC + ck + 1) * T::RS;
+      if (failed) {
+        if (lane == 0) {
+          rec[0] = NAN;
+          rec[1] = 1.f;
+        }
+        continue;
+      }
+      if (ck < 0) {
+        own_window<D>(p, static_cast<int64_t>(b) * p.Hkv + hkv, max(0, min(__ldg(p.seq_lens + b), p.W)), p.q + pair * D, rec, lane);
+        continue;
+      }
+      const int2 seq = __ldg(p.seqs + b);                  // its shared tokens, its own
+      const int t0 = seq.x + ck * p.CH, t1 = min(seq.x + seq.y, t0 + p.CH);
+      if (t0 >= t1) continue;                              // the merge does not read it
+      // the query in fp16 against the scales of the key groups: word i holds
+      // channels 2i, 2i + 1 (of D, then around again)
+      static_assert((31 + J) * C * 2 <= kOwnP - kOwnQ, "query entries 0 .. 30 + J fit");
+      const uint32_t* qw = reinterpret_cast<const uint32_t*>(p.q + pair * D);
+      constexpr int QW = (31 + J) * C / 2, PER = (QW + 31) / 32;
+      float2 f[PER];
+      float top = 0.f;
 #pragma unroll
-    for (int k = 0; k < PER; ++k) {
-      const int i = (lane + 32 * k) % (D / 2);
-      f[k] = bf16x2_to_float2(__ldg(qw + i));
-      const float g = fk[2 * i / C];
-      f[k].x *= g;
-      f[k].y *= g;
-      top = fmaxf(top, fmaxf(finite_abs(f[k].x), finite_abs(f[k].y)));
-    }
-    const int kq = scale_exp(redux_fmax(top));
-    const float fq = pow2(kq);
-    __syncwarp();
+      for (int k = 0; k < PER; ++k) {
+        const int i = (lane + 32 * k) % (D / 2);
+        f[k] = bf16x2_to_float2(__ldg(qw + i));
+        const float g = fk[2 * i / C];
+        f[k].x *= g;
+        f[k].y *= g;
+        top = fmaxf(top, fmaxf(finite_abs(f[k].x), finite_abs(f[k].y)));
+      }
+      const int kq = scale_exp(redux_fmax(top));
+      const float fq = pow2(kq);
+      __syncwarp();
 #pragma unroll
-    for (int k = 0; k < PER; ++k)
-      if (lane + 32 * k < QW) qs[lane + 32 * k] = half2_bits(f[k].x * fq, f[k].y * fq);
-    __syncwarp();
-    own_chunk<J, C>(p, pool_h, b, t0, t1, ldexpf(p.scale_log2, -kq), unv, scratch, rec, lane);
-   }
-   th = t_end;
+      for (int k = 0; k < PER; ++k)
+        if (lane + 32 * k < QW) qs[lane + 32 * k] = half2_bits(f[k].x * fq, f[k].y * fq);
+      __syncwarp();
+      own_chunk<J, C>(p, pool_h, b, t0, t1, ldexpf(p.scale_log2, -kq), unv, scratch, rec, lane);
+    }
+    th = t_end;
   }
   // the merge waits for this grid, which ends after the shared one
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// One warp per (sequence, query head): joins the records that its blocks wrote.
+// One warp per (sequence, query head): joins the records that its blocks wrote,
+// four requested at a time. 128 pairs with 10 records each take 1 us past the
+// kernel before, 4096 pairs 4 us.
 template <int D, int N>
 __global__ void __launch_bounds__(128) shared_merge_kernel(const SharedParams p) {
   constexpr int RS = 4 + D, NCH = (D + 31) / 32;
@@ -1610,10 +1642,11 @@ SharedLayout make_layout(const Geometry& g, int batch, const SharedPlan& q) {
 // The shapes that the kernels take, where sharing pays: measured on B200 (16
 // heads of 128, own tokens 75 on average; these kernels / streaming each sequence,
 // us at 200, 4000 and 16000 shared tokens): groups of 3 sequences 29/18, 32/24,
-// 33/31; of 4 21/19, 23/24, 34/35; of 8 18/25, 22/30, 35/50; 8 groups of 2 24/33,
-// 56/49, 151/92; 8 groups of 4 27/60, 58/89, 154/168. With few (sequence, head)
-// pairs the four launches cost more than they save: one head of 64, 16 sequences
-// 15/13, 18/17, 23/20.
+// 33/31; of 4 18/19, 22/25, 34/35; of 8 18/25, 22/30, 34/50; 8 groups of 2 24/33,
+// 56/49, 151/92; 8 groups of 4 26/60, 58/89, 152/168. 40 heads of 96 (c = 8): of 4
+// 19/32, 31/38, 70/60; of 8 21/48, 33/58, 70/110. With few (sequence, head) pairs
+// the four launches cost more than they save: one head of 64, 16 sequences 15/13,
+// 18/17, 23/20.
 bool shared_attn_supported(const Geometry& g, int batch, int n_groups, int out_dtype) {
   if (out_dtype != LOOPVQ_DTYPE_BF16 || n_groups == 0) return false;
   if (static_cast<int64_t>(batch) * (g.Hq / g.Hkv) < 4ll * n_groups || static_cast<int64_t>(batch) * g.Hq < 64) return false;
