@@ -467,7 +467,8 @@ loopvq_status loopvq_prefill_attn(const loopvq_config* cfg, int layer, int loop_
  * nothing; one with fewer quantised tokens than shared_lens[i] uses the first
  * of them.
  *
- *  group_starts  int32 [n_groups + 1], ascending, in [0, batch].
+ *  group_starts  int32 [n_groups + 1], ascending, in [0, batch]; n_groups is
+ *                at most batch.
  *  shared_lens   int32 [n_groups], shared quantised tokens of each group.
  *  max_group, max_shared_len, max_own_len
  *                bounds on the host: sequences of a group, shared quantised
@@ -481,9 +482,9 @@ loopvq_status loopvq_prefill_attn(const loopvq_config* cfg, int layer, int loop_
  *
  * Two forms, chosen per call:
  *  - bf16 output, (J, c) = (32, 4), (16, 4), (12, 8), (16, 8) or (24, 4), on
- *    average at least four query rows (sequences times Hq/Hkv) per group and
- *    at least 64 (sequence, query head) pairs: the tensor-core form. Shared
- *    tokens are dequantised once per group and kv-head. Codewords and softmax
+ *    average at least four query rows (sequences times Hq/Hkv) per group, at
+ *    least 64 (sequence, query head) pairs, sm_scale in [2^-20, 2^20]: the
+ *    tensor-core form. Shared tokens are dequantised once per group and kv-head. Codewords and softmax
  *    weights enter the products in fp16 (half a step is 2^-11 relative; both are
  *    scaled by powers of two first), sums are float32, so a score, and lse, is
  *    within about 2^-11 sm_scale sum |q_i k_i|. group_starts that do not ascend

@@ -1646,8 +1646,10 @@ SharedLayout make_layout(const Geometry& g, int batch, const SharedPlan& q) {
 // 56/49, 151/92; 8 groups of 4 26/60, 58/89, 152/168. 40 heads of 96 (c = 8): of 4
 // 19/32, 31/38, 70/60; of 8 21/48, 33/58, 70/110. With few (sequence, head) pairs
 // the four launches cost more than they save: one head of 64, 16 sequences 15/13,
-// 18/17, 23/20.
-bool shared_attn_supported(const Geometry& g, int batch, int n_groups, int out_dtype) {
+// 18/17, 23/20. The factor of a score is sm_scale log2(e) 2^-kq, |kq| <= 100 (the
+// queries' power of two): outside 2^-20 .. 2^20 it could leave float32's range.
+bool shared_attn_supported(const Geometry& g, int batch, int n_groups, int out_dtype, float sm_scale) {
+  if (!(sm_scale >= 0x1p-20f && sm_scale <= 0x1p20f)) return false;
   if (out_dtype != LOOPVQ_DTYPE_BF16 || n_groups == 0) return false;
   if (static_cast<int64_t>(batch) * (g.Hq / g.Hkv) < 4ll * n_groups || static_cast<int64_t>(batch) * g.Hq < 64) return false;
   switch (g.J * 100 + g.c) {

@@ -82,6 +82,28 @@ def test_large_and_small_scores(q_scale):
     check_shared(c, *c.run_gpu())
 
 
+@pytest.mark.parametrize("sm_scale,q_scale", [(1e-38, 1.0), (1e-20, 1e-30), (2.0 ** -20, 1e-30), (2.0 ** 20, 1e-7),
+                                              (1e25, 1e-26)])
+def test_scales_far_from_one(sm_scale, q_scale):
+    # one sequence's queries are zero: all of its tokens weigh the same
+    c = SharedCase(H16, [(4, 300)], [40, 2, 100, 0], q_scale=q_scale, seed=15)
+    c.sm_scale = sm_scale
+    c.q[2] = 0
+    check_shared(c, *c.run_gpu())
+
+
+def test_own_tokens_of_many_pairs():
+    # chunks of 512 tokens: 32 sequences of 16 heads, ends on either side of them
+    own = [0, 1, 255, 256, 257, 511, 512, 513, 700, 1023, 1024, 1025] + [i * 29 % 600 for i in range(20)]
+    c = SharedCase(H16, [(20, 300), (10, 90)], own, seed=21)
+    check_shared(c, *c.run_gpu(), pairs=sample_pairs(c.B, 16, 60, 5, whole=(7,)))
+
+
+def test_own_tokens_of_more_than_sixty_four_chunks():
+    c = SharedCase(H16, [(4, 300)], [17000, 16640, 100, 0], seed=22)
+    check_shared(c, *c.run_gpu(), pairs=sample_pairs(c.B, 16, 24, 6))
+
+
 @pytest.mark.parametrize("k_scale,v_scale", [(1e-6, 1e5), (3e4, 1e-7)])
 def test_codebooks_far_from_one(k_scale, v_scale):
     c = SharedCase(H16, [(4, 300)], [40, 2, 100, 0], q_scale=1e-4 if k_scale > 1 else 1.0, seed=6)
