@@ -476,8 +476,10 @@ loopvq_status loopvq_prefill_attn(const loopvq_config* cfg, int layer, int loop_
  *                shared ones.
  *  workspace     at least loopvq_decode_shared_workspace_bytes(cfg, batch,
  *                n_groups, max_group, max_shared_len, max_own_len) bytes,
- *                16-byte aligned; the status word as for loopvq_decode_attn.
- *                Calls that may overlap need workspaces of their own.
+ *                16-byte aligned; the status word as for loopvq_decode_attn. No
+ *                smaller batch, count or bound needs more, so one made for the
+ *                largest call serves the others. Calls that may overlap need
+ *                workspaces of their own.
  * Every other argument as for loopvq_decode_attn; codebooks must be finite.
  *
  * Two forms, chosen per call:

@@ -423,7 +423,7 @@ size_t loopvq_decode_shared_workspace_bytes(const loopvq_config* cfg, int batch,
     return 0;
   // enough for either form, so that the size does not depend on the output type
   return std::max(loopvq::decode_workspace_bytes(batch * g.Hq, g.J, g.d),
-                  loopvq::shared_attn_workspace_bytes(g, batch, n_groups, max_group, max_shared_len, max_own_len));
+                  loopvq::shared_attn_workspace_bytes(g, batch, max_own_len));
 }
 
 loopvq_status loopvq_decode_attn_shared(const loopvq_config* cfg, int layer, int loop_step,

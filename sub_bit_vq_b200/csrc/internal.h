@@ -96,8 +96,7 @@ struct SharedArgs {
   void* stream;
 };
 bool shared_attn_supported(const Geometry& g, int batch, int n_groups, int out_dtype, float sm_scale);
-size_t shared_attn_workspace_bytes(const Geometry& g, int batch, int n_groups, int max_group, int max_shared,
-                                   int max_own);
+size_t shared_attn_workspace_bytes(const Geometry& g, int batch, int max_own);
 loopvq_status launch_shared_attn(const SharedArgs& a);
 
 struct EncodeArgs {

@@ -342,7 +342,8 @@ __device__ __forceinline__ int group_shared(const SharedParams& p, int g) {
 constexpr int kSetupTiles = 5;
 
 struct Group {
-  int lo, rows, S, tiles, cost;   // first sequence, query rows, shared tokens and tiles, cost of its row tiles per head
+  int lo, rows, S, tiles;         // first sequence, query rows, shared tokens and tiles
+  int64_t cost;                   // of its row tiles per head
 };
 template <int TOK, int N>
 __device__ __forceinline__ Group group_info(const SharedParams& p, int g) {
@@ -352,7 +353,7 @@ __device__ __forceinline__ Group group_info(const SharedParams& p, int g) {
     r.rows = max(0, min(min(p.B, __ldg(p.group_starts + g + 1)) - r.lo, p.max_group)) * p.ratio;
     r.S = group_shared(p, g);
     r.tiles = (r.S + TOK - 1) / TOK;
-    r.cost = r.tiles > 0 ? (r.rows + N - 1) / N * (r.tiles + kSetupTiles) : 0;
+    r.cost = r.tiles > 0 ? static_cast<int64_t>((r.rows + N - 1) / N) * (r.tiles + kSetupTiles) : 0;
   }
   return r;
 }
@@ -407,10 +408,11 @@ __device__ void plan_walks(const SharedParams& p) {
           if (before + incl[mid] > x) z = mid; else a = mid + 1;
         }
         const Group r = group_info<TOK, N>(p, g0 + a);
-        const int off = static_cast<int>(x - before - (a > 0 ? incl[a - 1] : 0)), cost = r.tiles + kSetupTiles;
+        const int64_t off = x - before - (a > 0 ? incl[a - 1] : 0);
+        const int cost = r.tiles + kSetupTiles;
         w.g = g0 + a;
-        w.rt = off / cost;
-        w.pos = off - w.rt * cost;
+        w.rt = static_cast<int>(off / cost);
+        w.pos = static_cast<int>(off % cost);
         w.lo = r.lo;
         w.rows = r.rows;
         w.S = r.S;
@@ -1407,8 +1409,9 @@ __global__ void __launch_bounds__(kOwnWarps * 32, 1) shared_own_kernel(const Sha
         continue;
       }
       const int2 seq = __ldg(p.seqs + b);                  // its shared tokens, its own
-      const int t0 = seq.x + ck * p.CH, t1 = min(seq.x + seq.y, t0 + p.CH);
-      if (t0 >= t1) continue;                              // the merge does not read it
+      const int c0 = ck * p.CH;
+      if (c0 >= seq.y) continue;                           // the merge does not read it
+      const int t0 = seq.x + c0, t1 = t0 + min(seq.y - c0, p.CH);
       // the query in fp16 against the scales of the key groups: word i holds
       // channels 2i, 2i + 1 (of D, then around again)
       static_assert((31 + J) * C * 2 <= kOwnP - kOwnQ, "query entries 0 .. 30 + J fit");
@@ -1502,15 +1505,18 @@ struct SharedPlan {
   int N, NC, CH, shared_blocks, own_blocks;
 };
 constexpr int kPlanSms = 148;             // blocks that run at once (one per SM of a B200)
+constexpr int kOwnChunk = 256;            // own tokens of a task at least, and chunks of a pair at most
+constexpr int kMaxChunks = 64;
 
 SharedPlan make_plan(const Geometry& g, int batch, int n_groups, int max_group, int max_shared, int max_own) {
   SharedPlan q{};
   const int ratio = g.Hq / g.Hkv;
   const int64_t rows = static_cast<int64_t>(max_group) * ratio;
   q.N = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-  q.CH = static_cast<int64_t>(batch) * g.Hq >= 512 ? 512 : 256;
-  while ((max_own + q.CH - 1) / q.CH > 64) q.CH *= 2;
-  q.NC = 1 + (max_own + q.CH - 1) / q.CH;                  // the window, and the chunks
+  q.CH = static_cast<int64_t>(batch) * g.Hq >= 512 ? 2 * kOwnChunk : kOwnChunk;
+  auto chunks = [&] { return max_own / q.CH + (max_own % q.CH != 0 ? 1 : 0); };
+  while (chunks() > kMaxChunks) q.CH *= 2;
+  q.NC = 1 + chunks();                                     // the window, and the chunks
   // Both grids together fill the machine once. The own grid gets the number of
   // blocks with which the later of the two ends first, by measured times (SM
   // cycles): a tile; a block's 16 warps' way through a task each, which grows with
@@ -1518,7 +1524,7 @@ SharedPlan make_plan(const Geometry& g, int batch, int n_groups, int max_group, 
   // more of them where blocks start and end inside heads. (Own tokens, and the
   // shared ones of several groups, as if spread over the upper half of their range.)
   const double t_tile = q.N == 16 ? 2200 : q.N == 32 ? 2700 : 3400;
-  const int tiles = (max_shared + 4 * g.LB - 1) / (4 * g.LB);
+  const int tiles = max_shared / (4 * g.LB) + 1;
   const int64_t of_rows = n_groups * ((rows + q.N - 1) / q.N), of_batch = n_groups + static_cast<int64_t>(batch) * ratio / q.N;
   const double units = max_shared > 0 ? static_cast<double>(of_rows < of_batch ? of_rows : of_batch) * g.Hkv : 0;
   const int64_t tasks = static_cast<int64_t>(batch) * g.Hq * q.NC;
@@ -1619,19 +1625,22 @@ loopvq_status launch_shared_jc(const SharedParams& p, int N, cudaStream_t st) {
   }
 }
 
-// Byte offsets of the workspace's parts.
+// Byte offsets of the workspace's parts, with room for every way make_plan may
+// cut up a call of at most these sizes: a workspace made for a larger batch or
+// more own tokens serves a smaller call.
 struct SharedLayout {
   size_t srec, orec, tables, exps, walks, spans, seqs, end;
 };
-SharedLayout make_layout(const Geometry& g, int batch, const SharedPlan& q) {
+SharedLayout make_layout(const Geometry& g, int batch, int max_own) {
   const size_t rec = (4 + static_cast<size_t>(g.d)) * sizeof(float), pairs = static_cast<size_t>(batch) * g.Hq;
+  const int chunks = max_own / kOwnChunk + (max_own % kOwnChunk != 0 ? 1 : 0);
   SharedLayout w;
   w.srec = kStatusBytes;
-  w.orec = w.srec + (q.shared_blocks > 0 ? pairs + static_cast<size_t>(q.shared_blocks) * q.N : 0) * rec;
-  w.tables = w.orec + pairs * q.NC * rec;
+  w.orec = w.srec + (pairs + static_cast<size_t>(kPlanSms) * kMaxRows) * rec;
+  w.tables = w.orec + pairs * (1 + std::min(chunks, kMaxChunks)) * rec;
   w.exps = w.tables + static_cast<size_t>(g.Hkv) * 2 * kTabBytes;
   w.walks = w.exps + static_cast<size_t>(g.Hkv) * 64 * sizeof(int);
-  w.spans = w.walks + static_cast<size_t>(q.shared_blocks) * sizeof(Walk);
+  w.spans = w.walks + static_cast<size_t>(kPlanSms) * sizeof(Walk);
   w.seqs = w.spans + pairs * sizeof(int2);
   w.end = w.seqs + static_cast<size_t>(batch) * sizeof(int2);
   return w;
@@ -1658,16 +1667,17 @@ bool shared_attn_supported(const Geometry& g, int batch, int n_groups, int out_d
   }
 }
 
-size_t shared_attn_workspace_bytes(const Geometry& g, int batch, int n_groups, int max_group, int max_shared,
-                                   int max_own) {
-  return make_layout(g, batch, make_plan(g, batch, n_groups, max_group, max_shared, max_own)).end;
+size_t shared_attn_workspace_bytes(const Geometry& g, int batch, int max_own) {
+  return make_layout(g, batch, max_own).end;
 }
 
 loopvq_status launch_shared_attn(const SharedArgs& a) {
   const Geometry& g = *a.geo;
   const SharedPlan q = make_plan(g, a.batch, a.n_groups, a.max_group, a.max_shared, a.max_own);
-  // (records and tasks are counted in 32 bits)
-  if (static_cast<int64_t>(a.batch) * g.Hq * q.NC > INT_MAX / 2) return LOOPVQ_ERR_UNSUPPORTED;
+  // (records, tasks and a sequence's tokens are counted in 32 bits)
+  if (static_cast<int64_t>(a.batch) * g.Hq * q.NC > INT_MAX / 2 ||
+      static_cast<int64_t>(a.max_shared) + a.max_own > INT_MAX / 2)
+    return LOOPVQ_ERR_UNSUPPORTED;
   const int gamma = a.loop_step / g.g, tau = a.loop_step % g.g;
   SharedParams p{};
   p.q = static_cast<const uint16_t*>(a.q);
@@ -1686,7 +1696,7 @@ loopvq_status launch_shared_attn(const SharedArgs& a) {
   p.win_v = static_cast<const uint16_t*>(a.win_v);
   char* ws = static_cast<char*>(a.workspace);
   p.status = reinterpret_cast<int*>(ws);
-  const SharedLayout w = make_layout(g, a.batch, q);
+  const SharedLayout w = make_layout(g, a.batch, a.max_own);
   p.srec = reinterpret_cast<float*>(ws + w.srec);
   p.orec = reinterpret_cast<float*>(ws + w.orec);
   p.tables = reinterpret_cast<unsigned char*>(ws + w.tables);

@@ -260,6 +260,22 @@ def test_other_stream_replay_and_repeat():
     assert int(ws[:4].view(torch.int32)) == 0
 
 
+def test_one_workspace_serves_calls_of_every_size_and_form():
+    cases = [SharedCase(H16, [(40, 500)], [i * 17 % 600 for i in range(40)], seed=61),
+             SharedCase(H16, [(4, 300)], [700, 0, 1, 2], seed=62), SharedCase(H16, [(2, 300)], [70, 0], seed=63),
+             SharedCase(H16, [(9, 64), (3, 200)], [3] * 12, seed=64)]
+    ws = torch.zeros(max(c.workspace_bytes() for c in cases), dtype=torch.uint8, device="cuda")
+    want = [(c.run_gpu()[0], c.run_gpu(out_dtype=torch.float32)[0]) for c in cases]
+    for i in (0, 1, 2, 3, 1, 0):
+        c, d = cases[i], cases[i].device()
+        for dtype, w in zip((torch.bfloat16, torch.float32), want[i]):
+            o = torch.full((c.B, 16, 128), float("nan"), dtype=dtype, device="cuda")
+            L.loopvq_decode_attn_shared(c.config(), 0, c.t, **d, out=o, workspace=ws, max_group=c.max_group,
+                                        max_shared_len=c.max_shared, max_own_len=c.max_own, sm_scale=c.sm_scale)
+            np.testing.assert_array_equal(o.float().cpu().numpy(), w)
+    assert int(ws[:4].view(torch.int32)) == 0
+
+
 def test_two_calls_at_once_with_workspaces_of_their_own():
     cases = [SharedCase(H16, [(5, 1500)], [40, 0, 77, 3, 150], seed=31), SharedCase(H16, [(6, 900)], [4, 0, 7, 3, 15, 90], seed=32)]
     want = [c.run_gpu()[0] for c in cases]

@@ -2,6 +2,7 @@
 workspace sizes, the binding's checks."""
 
 import os
+import random
 import re
 
 import pytest
@@ -51,6 +52,19 @@ def test_workspace_is_checked_and_grows():
     assert L.loopvq_decode_shared_workspace_bytes(cfg, 4, 2, 3, 5 * 64 + 1, 0) == 0
     assert L.loopvq_decode_shared_workspace_bytes(cfg, 2, 1, 2, 200, 100) <= need
     assert L.loopvq_decode_shared_workspace_bytes(cfg, 2, 0, 0, 0, 100) > 0
+
+
+def test_a_workspace_of_the_largest_call_serves_smaller_ones():
+    cfg = _cfg(n_kv_heads=8, n_q_heads=16, n_pages=2000, max_batch=80, max_pages_per_seq=1500)
+    size = lambda *a: L.loopvq_decode_shared_workspace_bytes(cfg, *a)
+    r = random.Random(3)
+    for _ in range(300):
+        b, ms, mo = r.randint(1, 80), r.randint(0, 60000), r.choice([0, 255, 513, 16385, r.randint(1, 90000)])
+        ng = r.randint(0, b)
+        mg = r.randint(1, b)
+        b2 = r.randint(1, b)
+        less = (b2, r.randint(0, min(ng, b2)), r.randint(1, min(mg, b2)), r.randint(0, ms), r.randint(0, mo))
+        assert 0 < size(*less) <= size(b, ng, mg, ms, mo), (less, (b, ng, mg, ms, mo))
 
 
 def test_binding_checks_shapes_types_and_device():
