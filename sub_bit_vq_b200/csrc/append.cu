@@ -26,7 +26,7 @@
 // 133.7, 142.4 and 190 us against 132.9 on 32768 tokens: more registers, fewer
 // resident warps) and streams past the caches (138.4 us without the hints).
 // Measured on B200, 16 + 2 x 16 heads of 128: 32768 tokens in 132.9 us
-// (809 MB, 6.1 TB/s, 93% of the measured copy rate); one token of 8 and 256
+// (822 MB, 6.2 TB/s, 94% of the measured copy rate); one token of 8 and 256
 // sequences in 2.6 and 3.3 us.
 
 #include "common.cuh"

@@ -60,7 +60,10 @@
 // more and smaller ones lose); values handed over block by block (73: polls queue
 // behind the fill's accesses); one team filling both planes (61); products issued
 // by a warp of each fill team instead of one of their own, with 16 softmax warps at
-// 64 rows (61, and 233 for the 256 sequences).
+// 64 rows (61, and 233 for the 256 sequences); half a tile filled under the other
+// half's products, keys by channels and values by tokens (61 and 243; values only
+// 62 and 235): the products slow down under the same plane's fill, and there are
+// twice the hand-overs.
 
 #include <cuda_fp16.h>
 #include <math.h>
@@ -1511,8 +1514,24 @@ constexpr int kMaxChunks = 64;
 SharedPlan make_plan(const Geometry& g, int batch, int n_groups, int max_group, int max_shared, int max_own) {
   SharedPlan q{};
   const int ratio = g.Hq / g.Hkv;
-  const int64_t rows = static_cast<int64_t>(max_group) * ratio;
-  q.N = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  // Query rows of a block: the width whose row tiles cost least by the measured
+  // times of a tile (SM cycles). Of several groups the host knows the largest and
+  // the sum: half a row tile of each is taken as empty. (61 sequences in 7 uneven
+  // groups, 2 query heads a head: 65 us with 32 rows, 69 with the 64 that the
+  // largest group fills.)
+  const int64_t most = static_cast<int64_t>(max_group) * ratio, all = static_cast<int64_t>(batch) * ratio;
+  double units = 0, t_tile = 0;
+  for (int n = 16; n <= kMaxRows; n *= 2) {
+    const double cap = static_cast<double>(n_groups) * ((most + n - 1) / n);
+    const double u = n_groups > 1 ? std::min(cap, std::max<double>(n_groups, 0.5 * n_groups + static_cast<double>(all) / n)) : cap;
+    const double t = n == 16 ? 2200 : n == 32 ? 2700 : 3400;
+    if (q.N == 0 || u * t < units * t_tile) {
+      q.N = n;
+      units = u;
+      t_tile = t;
+    }
+  }
+  units = max_shared > 0 ? units * g.Hkv : 0;
   q.CH = static_cast<int64_t>(batch) * g.Hq >= 512 ? 2 * kOwnChunk : kOwnChunk;
   auto chunks = [&] { return max_own / q.CH + (max_own % q.CH != 0 ? 1 : 0); };
   while (chunks() > kMaxChunks) q.CH *= 2;
@@ -1523,10 +1542,7 @@ SharedPlan make_plan(const Geometry& g, int batch, int n_groups, int max_group, 
   // its tokens; the tables of a head and the warps that run out of its tasks first,
   // more of them where blocks start and end inside heads. (Own tokens, and the
   // shared ones of several groups, as if spread over the upper half of their range.)
-  const double t_tile = q.N == 16 ? 2200 : q.N == 32 ? 2700 : 3400;
   const int tiles = max_shared / (4 * g.LB) + 1;
-  const int64_t of_rows = n_groups * ((rows + q.N - 1) / q.N), of_batch = n_groups + static_cast<int64_t>(batch) * ratio / q.N;
-  const double units = max_shared > 0 ? static_cast<double>(of_rows < of_batch ? of_rows : of_batch) * g.Hkv : 0;
   const int64_t tasks = static_cast<int64_t>(batch) * g.Hq * q.NC;
   const double t_task = 1500 + 125 * (g.W + 0.75 * max_own * 32 / g.LB) / q.NC;
   const int64_t fit_b = (tasks + 15) / 16 > g.Hkv ? (tasks + 15) / 16 : g.Hkv;
