@@ -53,7 +53,8 @@
 // Measured 2200 and 3400 (1900 MHz): 52.5 us for those 8 sequences, of which 47 in
 // the shared grid (7 of them before its first tile), 5 + 1 around it in the tables
 // and the merge, against 77.9 us when every sequence streams on its own; 256
-// sequences over 16312 tokens 200 us against 1313.
+// sequences over 16312 tokens 187 us against 1313 (205 with the weights computed
+// only once P's buffer is free: with 64 rows there is one).
 //
 // What lost: the keys in two half tiles of M = 64 (71 us for the 8 sequences: a
 // product takes 90-150 cycles of issue under the fill's accesses, 47 alone, so
@@ -560,7 +561,7 @@ __device__ __forceinline__ int64_t pair_of(const SharedParams& p, const Segment&
 template <int J, int C, int N>
 __device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const Segment& u, uint32_t tmem) {
   using T = Shape<J, C>;
-  constexpr int D = T::D, NC = N / 2, CW = NC < 16 ? NC : 16;
+  constexpr int D = T::D, NC = N / 2;
   // P: rows of 64 query rows and one buffer, or of 32 and two (the same bytes)
   constexpr int PP = N > 32 ? 128 : 64, PB = N > 32 ? 1 : 2;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -779,48 +780,42 @@ __device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const S
     float l[NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) l[c] = 0.f;
-    float4 m4[NC / 4];                                     // this half's references
+    // this half's references: in shared memory, but for 16 rows in registers (more
+    // rows spilled: 100 us against 96 with 32 rows, 40 heads and 16312 tokens)
+    float4 m4[N > 16 ? 1 : NC / 4];
 #pragma unroll
-    for (int c = 0; c < NC / 4; ++c) m4[c] = make_float4(kUnset, kUnset, kUnset, kUnset);
+    for (int c = 0; c < (N > 16 ? 1 : NC / 4); ++c) m4[c] = make_float4(kUnset, kUnset, kUnset, kUnset);
+    auto refs = [&](int c) { return N > 16 ? *reinterpret_cast<const float4*>(m_ref + c0 + c) : m4[c / 4]; };
 #pragma unroll 1
     for (int i = 0; i < nt; ++i) {
-      failed = !mbar_wait(bar(kBarS0 + (i & 1)), (i >> 1) & 1, kShSpin);
+      failed = !mbar_wait(bar(kBarS0 + (i & 1)), (i >> 1) & 1, kShSpin) || failed;
       __syncwarp();
       tc_after();
       const int nv = nvs[(i & 3) * 4 + quad];
       const bool masked = tok0 + (i + 1) * T::TOK > min_lim;   // some row ends inside this tile
       const int tok = tok0 + i * T::TOK + quad * T::LB + lane;
-      // CW columns of this token's scores, -inf where there is none (read again for
-      // each use when the half has more than CW: registers)
-      auto scores = [&](int c, uint32_t (&sv)[CW]) {
-        tld<CW>(lanes + kTmS + (i & 1) * 64 + c0 + c, sv);
-        tld_wait();
-        if (nv < 32 && lane >= nv) {                       // no token in this slot
+      // this token's scores, -inf where there is none
+      uint32_t sv[NC];
+      tld<NC>(lanes + kTmS + (i & 1) * 64 + c0, sv);
+      tld_wait();
+      if (nv < 32 && lane >= nv) {                         // no token in this slot
 #pragma unroll
-          for (int k = 0; k < CW; ++k) sv[k] = 0xff800000u;
-        }
-        if (masked) {
+        for (int c = 0; c < NC; ++c) sv[c] = 0xff800000u;
+      }
+      if (masked) {
 #pragma unroll
-          for (int k = 0; k < CW; ++k)
-            if (tok >= lim[c0 + c + k]) sv[k] = 0xff800000u;
-        }
-      };
-      uint32_t sv[CW];
+        for (int c = 0; c < NC; ++c)
+          if (tok >= lim[c0 + c]) sv[c] = 0xff800000u;
+      }
       float mx = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < NC; c += CW) {
-        scores(c, sv);
-#pragma unroll
-        for (int k = 0; k < CW; k += 4) {
-          const float4 mm = m4[(c + k) / 4];
-          mx = fmaxf(mx, fmaxf(fmaf(__uint_as_float(sv[k]), scale, -mm.x), fmaf(__uint_as_float(sv[k + 1]), scale, -mm.y)));
-          mx = fmaxf(mx, fmaxf(fmaf(__uint_as_float(sv[k + 2]), scale, -mm.z),
-                               fmaf(__uint_as_float(sv[k + 3]), scale, -mm.w)));
-        }
+      for (int c = 0; c < NC; c += 4) {
+        const float4 mm = refs(c);
+        mx = fmaxf(mx, fmaxf(fmaf(__uint_as_float(sv[c]), scale, -mm.x), fmaf(__uint_as_float(sv[c + 1]), scale, -mm.y)));
+        mx = fmaxf(mx, fmaxf(fmaf(__uint_as_float(sv[c + 2]), scale, -mm.z), fmaf(__uint_as_float(sv[c + 3]), scale, -mm.w)));
       }
-      if (i >= PB) failed = !mbar_wait(bar(kBarO0 + ((i - PB) & 1)), ((i - PB) >> 1) & 1, kShSpin) || failed;
       if (named_or(bar_id, 128, mx > kRaise || failed)) {
-        if (PB == 2 && i > 0) failed = !mbar_wait(bar(kBarO0 + ((i - 1) & 1)), ((i - 1) >> 1) & 1, kShSpin) || failed;
+        if (i > 0) failed = !mbar_wait(bar(kBarO0 + ((i - 1) & 1)), ((i - 1) >> 1) & 1, kShSpin) || failed;
         if (named_or(bar_id, 128, failed)) {               // uniform over the four warps
           failed = true;
           break;
@@ -831,13 +826,9 @@ __device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const S
         // keeps column c's maximum over the warp's tokens.
         float top = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < NC; c += CW) {
-          if (NC > CW) scores(c, sv);
-#pragma unroll
-          for (int k = 0; k < CW; ++k) {
-            const float t = redux_fmax(__uint_as_float(sv[k]) * scale);
-            if (lane == c + k) top = t;
-          }
+        for (int c = 0; c < NC; ++c) {
+          const float t = redux_fmax(__uint_as_float(sv[c]) * scale);
+          if (lane == c) top = t;
         }
         if (lane < NC) cm[quad * kMaxRows + c0 + lane] = top;
         named_sync(bar_id, 128);
@@ -851,7 +842,7 @@ __device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const S
         named_sync(bar_id, 128);                           // references and factors written; cm is free
 #pragma unroll
         for (int c = 0; c < NC; c += 4) {
-          m4[c / 4] = *reinterpret_cast<const float4*>(m_ref + c0 + c);
+          if (N <= 16) m4[c / 4] = *reinterpret_cast<const float4*>(m_ref + c0 + c);
           const float4 f = *reinterpret_cast<const float4*>(al + c0 + c);
           l[c] *= f.x;
           l[c + 1] *= f.y;
@@ -872,31 +863,29 @@ __device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const S
         }
         named_sync(bar_id, 128);                           // the factors are read
       }
+      // the weights, in registers until the products that read P's buffer are done
+      uint32_t w[NC / 2];
+#pragma unroll
+      for (int c = 0; c < NC; c += 4) {
+        const float4 mm = refs(c);
+        const float e0 = fast_exp2(fmaf(__uint_as_float(sv[c]), scale, -mm.x));
+        const float e1 = fast_exp2(fmaf(__uint_as_float(sv[c + 1]), scale, -mm.y));
+        const float e2 = fast_exp2(fmaf(__uint_as_float(sv[c + 2]), scale, -mm.z));
+        const float e3 = fast_exp2(fmaf(__uint_as_float(sv[c + 3]), scale, -mm.w));
+        l[c] += e0;
+        l[c + 1] += e1;
+        l[c + 2] += e2;
+        l[c + 3] += e3;
+        w[c / 2] = half2_bits(e0, e1);
+        w[c / 2 + 1] = half2_bits(e2, e3);
+      }
+      if (i >= PB) failed = !mbar_wait(bar(kBarO0 + ((i - PB) & 1)), ((i - PB) >> 1) & 1, kShSpin) || failed;
       unsigned char* prow = sm + kPOff + (i % PB) * (kTileRows * PP) + row * PP;
       const int swz = PP == 128 ? row & 7 : (row >> 1) & 3;
 #pragma unroll
-      for (int cc = 0; cc < NC; cc += CW) {
-        if (NC > CW) scores(cc, sv);
-#pragma unroll
-        for (int c = 0; c < CW; c += 8) {
-          uint32_t w[4];
-#pragma unroll
-          for (int k = 0; k < 4; k += 2) {
-            const float4 mm = m4[(cc + c + 2 * k) / 4];
-            const float e0 = fast_exp2(fmaf(__uint_as_float(sv[c + 2 * k]), scale, -mm.x));
-            const float e1 = fast_exp2(fmaf(__uint_as_float(sv[c + 2 * k + 1]), scale, -mm.y));
-            const float e2 = fast_exp2(fmaf(__uint_as_float(sv[c + 2 * k + 2]), scale, -mm.z));
-            const float e3 = fast_exp2(fmaf(__uint_as_float(sv[c + 2 * k + 3]), scale, -mm.w));
-            l[cc + c + 2 * k] += e0;
-            l[cc + c + 2 * k + 1] += e1;
-            l[cc + c + 2 * k + 2] += e2;
-            l[cc + c + 2 * k + 3] += e3;
-            w[k] = half2_bits(e0, e1);
-            w[k + 1] = half2_bits(e2, e3);
-          }
-          *reinterpret_cast<uint4*>(prow + ((((c0 + cc + c) >> 3) ^ swz) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-      }
+      for (int c = 0; c < NC; c += 8)
+        *reinterpret_cast<uint4*>(prow + ((((c0 + c) >> 3) ^ swz) << 4)) =
+            make_uint4(w[c / 2], w[c / 2 + 1], w[c / 2 + 2], w[c / 2 + 3]);
       proxy_fence();
       tc_before();
       __syncwarp();
@@ -1524,7 +1513,7 @@ SharedPlan make_plan(const Geometry& g, int batch, int n_groups, int max_group, 
   for (int n = 16; n <= kMaxRows; n *= 2) {
     const double cap = static_cast<double>(n_groups) * ((most + n - 1) / n);
     const double u = n_groups > 1 ? std::min(cap, std::max<double>(n_groups, 0.5 * n_groups + static_cast<double>(all) / n)) : cap;
-    const double t = n == 16 ? 2200 : n == 32 ? 2700 : 3400;
+    const double t = n == 16 ? 2200 : n == 32 ? 2500 : 3400;
     if (q.N == 0 || u * t < units * t_tile) {
       q.N = n;
       units = u;
