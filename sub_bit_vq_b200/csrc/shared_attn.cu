@@ -433,7 +433,7 @@ __device__ void plan_walks(const SharedParams& p) {
 // own. Also the split of every sequence into shared and own tokens and, in a block
 // of its own, where the shared grid's blocks start. The shared grid's blocks start
 // meanwhile and wait for this grid. 16 heads of 128 read 4.2 MB and write 2.1 MB in
-// 5.4 us, a launch's latency and two dependent loads.
+// 5 us, a launch's latency and two dependent loads.
 template <int J, int C, int N>
 __global__ void __launch_bounds__(kE) shared_table_kernel(const float* cb_k, const float* cb_v, int64_t cb_stride_head,
                                                           unsigned char* tables, int* exps, const SharedParams p) {
