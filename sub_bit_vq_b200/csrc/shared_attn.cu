@@ -50,7 +50,7 @@
 // 32696 tokens: 33.5 MB, 5 us); the products are small. What a tile costs is
 // shared-memory accesses: 2 x 32 KB of lookups, as much of stores, and the
 // products' reads, 1650 cycles of 128 bytes with 16 query rows, 1900 with 64.
-// Measured 2200 and 3400 (1900 MHz): 52.5 us for those 8 sequences, of which 47 in
+// Measured 2200 and 3400 (1900 MHz): 53 us for those 8 sequences, of which 47 in
 // the shared grid (7 of them before its first tile), 5 + 1 around it in the tables
 // and the merge, against 77.9 us when every sequence streams on its own; 256
 // sequences over 16312 tokens 187 us against 1313 (205 with the weights computed
