@@ -328,13 +328,14 @@ __device__ __forceinline__ int seq_vq(const SharedParams& p, int b) {
   return max(0, min(__ldg(p.seq_lens + b) - p.W, p.max_pages_per_seq * p.Pg));
 }
 
-// Group of sequence b (-1: none); every lane of the warp calls it.
+// Group of sequence b (-1: none; else b is one of the rows that group_info
+// counts); every lane of the warp calls it.
 __device__ __forceinline__ int group_of(const SharedParams& p, int b, int lane) {
   int n = 0;
   for (int i = lane; i < p.n_groups; i += 32) n += __ldg(p.group_starts + 1 + i) <= b ? 1 : 0;
   const int g = __reduce_add_sync(0xffffffffu, n);
   if (g >= p.n_groups || b < __ldg(p.group_starts + g) || b >= __ldg(p.group_starts + g + 1)) return -1;
-  if (b - __ldg(p.group_starts + g) >= p.max_group) return -1;
+  if (b - max(0, __ldg(p.group_starts + g)) >= p.max_group) return -1;
   return g;
 }
 __device__ __forceinline__ int group_shared(const SharedParams& p, int g) {

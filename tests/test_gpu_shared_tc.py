@@ -293,6 +293,16 @@ def test_two_calls_at_once_with_workspaces_of_their_own():
         np.testing.assert_array_equal(o.float().cpu().numpy(), w)
 
 
+def test_starts_at_the_ends_of_int32():
+    # the first two sequences are the group that the bound leaves; nothing lies outside
+    flag = B.LOOPVQ_DECODE_STATUS_BAD_GROUP
+    c = SharedCase(H16, [(5, 500)], [60, 4, 60, 0, 60], seed=23)
+    d = c.device()
+    for starts in ([-2 ** 31, 5], [-2 ** 31, 2 ** 31 - 1], [0, 2 ** 31 - 1]):
+        d["group_starts"].copy_(torch.tensor(starts, dtype=torch.int32))
+        check_shared(c, *c.run_gpu(status=flag, dev_inputs=d, bounds=(2, 500, 560)))
+
+
 def test_waits_that_run_out_are_reported_and_the_context_stays_usable():
     # the short-wait build gives no wait a try: the call ends with the flag set and
     # poisoned outputs, nothing in flight
