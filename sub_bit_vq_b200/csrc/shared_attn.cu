@@ -325,7 +325,7 @@ __device__ __forceinline__ float finite_abs(float v) {
 
 // Quantised tokens of sequence b.
 __device__ __forceinline__ int seq_vq(const SharedParams& p, int b) {
-  return max(0, min(__ldg(p.seq_lens + b) - p.W, p.max_pages_per_seq * p.Pg));
+  return max(0, min(max(0, __ldg(p.seq_lens + b)) - p.W, p.max_pages_per_seq * p.Pg));
 }
 
 // Group of sequence b (-1: none; else b is one of the rows that group_info

@@ -293,6 +293,16 @@ def test_two_calls_at_once_with_workspaces_of_their_own():
         np.testing.assert_array_equal(o.float().cpu().numpy(), w)
 
 
+@pytest.mark.parametrize("length", [-1, -2 ** 31])
+def test_negative_lengths_are_empty_sequences(length):
+    c = SharedCase(H16, [(5, 300)], [60, 4, 60, 0, 60], seed=24)
+    d = c.device()
+    for b in (0, 2):                                       # the first one's table still names the prefix
+        d["seq_lens"][b] = length
+        c.seq_lens[b] = c.n_vq[b] = 0
+    check_shared(c, *c.run_gpu(dev_inputs=d))
+
+
 def test_starts_at_the_ends_of_int32():
     # the first two sequences are the group that the bound leaves; nothing lies outside
     flag = B.LOOPVQ_DECODE_STATUS_BAD_GROUP
