@@ -76,6 +76,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "group_span.h"
 #include "internal.h"
 #include "tcgen05.cuh"
 
@@ -334,9 +335,9 @@ __device__ __forceinline__ int group_of(const SharedParams& p, int b, int lane) 
   int n = 0;
   for (int i = lane; i < p.n_groups; i += 32) n += __ldg(p.group_starts + 1 + i) <= b ? 1 : 0;
   const int g = __reduce_add_sync(0xffffffffu, n);
-  if (g >= p.n_groups || b < __ldg(p.group_starts + g) || b >= __ldg(p.group_starts + g + 1)) return -1;
-  if (b - max(0, __ldg(p.group_starts + g)) >= p.max_group) return -1;
-  return g;
+  if (g >= p.n_groups) return -1;
+  const GroupSpan s = group_span(__ldg(p.group_starts + g), __ldg(p.group_starts + g + 1), p.B, p.max_group);
+  return b >= s.lo && b - s.lo < s.n ? g : -1;
 }
 __device__ __forceinline__ int group_shared(const SharedParams& p, int g) {
   return max(0, min(__ldg(p.shared_lens + g), p.max_shared));
@@ -354,8 +355,9 @@ template <int TOK, int N>
 __device__ __forceinline__ Group group_info(const SharedParams& p, int g) {
   Group r{0, 0, 0, 0, 0};
   if (g < p.n_groups) {
-    r.lo = max(0, __ldg(p.group_starts + g));
-    r.rows = max(0, min(min(p.B, __ldg(p.group_starts + g + 1)) - r.lo, p.max_group)) * p.ratio;
+    const GroupSpan s = group_span(__ldg(p.group_starts + g), __ldg(p.group_starts + g + 1), p.B, p.max_group);
+    r.lo = s.lo;
+    r.rows = s.n * p.ratio;
     r.S = group_shared(p, g);
     r.tiles = (r.S + TOK - 1) / TOK;
     r.cost = r.tiles > 0 ? static_cast<int64_t>((r.rows + N - 1) / N) * (r.tiles + kSetupTiles) : 0;
@@ -445,6 +447,7 @@ __global__ void __launch_bounds__(kE) shared_table_kernel(const float* cb_k, con
     const int id = (blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
     for (int g = id * kE + static_cast<int>(threadIdx.x); g < p.n_groups; g += blocks * kE) {
       const int lo = __ldg(p.group_starts + g), hi = __ldg(p.group_starts + g + 1), s = __ldg(p.shared_lens + g);
+      // (the difference is taken of ends inside [0, B] only)
       if ((lo < 0 || hi > p.B || hi < lo || hi - lo > p.max_group || s < 0 || s > p.max_shared) && p.status != nullptr)
         atomicOr(p.status, LOOPVQ_DECODE_STATUS_BAD_GROUP);
     }

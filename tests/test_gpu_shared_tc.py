@@ -313,6 +313,16 @@ def test_starts_at_the_ends_of_int32():
         check_shared(c, *c.run_gpu(status=flag, dev_inputs=d, bounds=(2, 500, 560)))
 
 
+@pytest.mark.parametrize("starts", [[0, -2 ** 31], [5, -2 ** 31], [2 ** 31 - 1, -2], [-2 ** 31, -1], [2 ** 31 - 1, 2 ** 31 - 1],
+                                    [4, 2]])
+def test_starts_that_leave_no_group(starts):
+    # no sequence is in a group: each reads all of its tokens as its own
+    c = SharedCase(H16, [(5, 500)], [60, 4, 60, 0, 60], seed=23)
+    d = c.device()
+    d["group_starts"].copy_(torch.tensor(starts, dtype=torch.int32))
+    check_shared(c, *c.run_gpu(status=B.LOOPVQ_DECODE_STATUS_BAD_GROUP, dev_inputs=d, bounds=(5, 500, 560)))
+
+
 def test_waits_that_run_out_are_reported_and_the_context_stays_usable():
     # the short-wait build gives no wait a try: the call ends with the flag set and
     # poisoned outputs, nothing in flight

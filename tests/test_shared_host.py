@@ -1,9 +1,11 @@
 """Host-side tests of loopvq_decode_attn_shared: refusals before any launch,
 workspace sizes, the binding's checks."""
 
+import ctypes
 import os
 import random
 import re
+import subprocess
 
 import pytest
 import torch
@@ -100,3 +102,27 @@ def test_status_bit_matches_the_header():
     text = open(os.path.join(ROOT, "include", "loopvq.h")).read()
     m = re.search(r"LOOPVQ_DECODE_STATUS_BAD_GROUP\s*=\s*(\d+)", text)
     assert int(m.group(1)) == B.LOOPVQ_DECODE_STATUS_BAD_GROUP == L.LOOPVQ_DECODE_STATUS_BAD_GROUP
+
+
+def test_a_group_is_a_part_of_the_batch_whatever_its_starts(tmp_path):
+    # the kernels' own arithmetic, compiled for the host: ends at and around the limits
+    # of int32 must not wrap into a group outside [0, batch)
+    src = tmp_path / "span.cpp"
+    src.write_text('#include "group_span.h"\n'
+                   'extern "C" void span(int s, int e, int b, int m, int* o) {\n'
+                   '  const loopvq::GroupSpan g = loopvq::group_span(s, e, b, m);\n  o[0] = g.lo; o[1] = g.n;\n}\n')
+    so = tmp_path / "span.so"
+    subprocess.run(["g++", "-O1", "-ftrapv", "-shared", "-fPIC", "-I", os.path.join(ROOT, "sub_bit_vq_b200", "csrc"),
+                    str(src), "-o", str(so)], check=True)
+    span = ctypes.CDLL(str(so)).span
+    ends = [-2 ** 31, -2 ** 31 + 1, -2 ** 30, -3, -1, 0, 1, 2, 4, 5, 6, 7, 2 ** 30, 2 ** 31 - 2, 2 ** 31 - 1]
+    out = (ctypes.c_int * 2)()
+    for batch in (1, 5, 2 ** 30):
+        for most in (1, 2, 5, batch):
+            for s in ends:
+                for e in ends:
+                    span(s, e, batch, most, out)
+                    lo, n = out
+                    want = range(max(s, 0), max(max(s, 0), min(e, batch)))[:most]
+                    assert 0 <= lo and 0 <= n <= most and lo + n <= batch, (s, e, batch, most, lo, n)
+                    assert range(lo, lo + n) == want, (s, e, batch, most, lo, n)   # (empty ranges are equal)
