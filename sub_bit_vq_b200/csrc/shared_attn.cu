@@ -772,7 +772,6 @@ __device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const S
                            (i > 0 || s > 0) ? 1u : 0u);
         tc_commit(bar(kBarO0 + (i & 1)));
       }
-      tc_commit(bar(kBarDrain));                           // everything issued so far
     }
     __syncwarp();
   } else {
@@ -931,8 +930,12 @@ __device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const S
   }
   const bool any_failed = __syncthreads_or(failed);
   if (any_failed) {
-    // a bounded wait gave up: wait for what was issued, flag, poison the records
+    // a bounded wait gave up: wait for what was issued, flag, poison the records.
+    // (The thread that issued the products commits them only here: every other
+    // arrival of a segment is waited for before its barriers are invalidated, and
+    // one that nobody waits for could come after.)
     if (tid == kMmaWarp * 32) {
+      tc_commit(bar(kBarDrain));
       const bool drained = mbar_wait(bar(kBarDrain), 0, kShDrainSpin) &&
                            (!u.load || (mbar_wait(bar(kBarTabK), 0, kShDrainSpin) && mbar_wait(bar(kBarTabV), 0, kShDrainSpin)));
       if (p.status != nullptr)
