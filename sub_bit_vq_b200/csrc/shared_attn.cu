@@ -42,9 +42,11 @@
 // are float32 over unrounded weights.
 //
 // Rounding. Keys, values and weights enter the products as fp16: half a step is
-// 2^-11 of each value, an eighth of the bf16 output's own. Codebooks and queries
-// are scaled by powers of two into fp16's range (exact), so their magnitude does
-// not matter. float32 outputs take the streaming kernels.
+// 2^-11 of each value, an eighth of the bf16 output's own. Codebooks are scaled by
+// powers of two into fp16's range, one per channel group, queries by one per unit or,
+// where its rows differ by more than 2^kRowSpan, one per row (exact but for
+// entries 2^-19 below their group's or row's largest). float32 outputs take the
+// streaming kernels.
 //
 // Cost. HBM has to deliver a group's indices once (8 sequences of 16 heads over
 // 32696 tokens: 33.5 MB, 5 us); the products are small. What a tile costs is
@@ -96,6 +98,11 @@ constexpr int kMaxRows = 64;              // query rows of a block
 constexpr float kRaise = 14.f;            // log2: a weight reaches 2^14 at most
 constexpr float kTop = 6.f;               // log2: weight of the maximum after a raise
 constexpr float kUnset = -1e30f;          // reference of a row that has seen no token
+// log2: how far the rows of a unit may differ and still share a scale. A row's
+// largest entry is then 2^5 at least in fp16, so what its smaller ones lose (half
+// of 2^-24) is 2^-30 of it. (A factor per row in every tile cost 3.9 us of 52.9
+// with 16 rows, 9 of 93 with 32.)
+constexpr int kRowSpan = 8;
 #ifndef LOOPVQ_TC_SPIN
 #define LOOPVQ_TC_SPIN (1 << 20)
 #endif
@@ -118,10 +125,10 @@ constexpr int kQBytes = kMaxRows * 256;
 constexpr int kMOff = kQOff + kQBytes;                     // float [64]: references
 constexpr int kCmOff = kMOff + kMaxRows * 4;               // float [4][64]: column maxima, then sums
 constexpr int kAlOff = kCmOff + 4 * kMaxRows * 4;          // float [64]: factors of a raise
-constexpr int kLimOff = kAlOff + kMaxRows * 4;             // int [64]: a row's shared tokens
+constexpr int kScOff = kAlOff + kMaxRows * 4;              // float [64]: a row's 2^-kq, when the rows differ
+constexpr int kLimOff = kScOff + kMaxRows * 4;             // int [64]: a row's shared tokens
 constexpr int kNvOff = kLimOff + kMaxRows * 4;             // int [4 tiles][4 blocks]: valid slots
-constexpr int kRedOff = kNvOff + 64;                       // float [25]: block reduction
-constexpr int kBarOff = kRedOff + 112;                     // mbarriers
+constexpr int kBarOff = kNvOff + 64;                       // mbarriers
 constexpr int kSegOff = kBarOff + 96;                      // the block's segment and walk
 constexpr int kTmemSlotOff = kSegOff + 144;
 constexpr int kShSmem = kTmemSlotOff + 16;
@@ -308,17 +315,6 @@ __device__ __forceinline__ int scale_exp(float top) {
   return max(-100, min(100, 13 - ilogbf(top)));
 }
 
-// Largest finite magnitude over the block (every thread calls it).
-__device__ __forceinline__ float block_max(float v, float* red, int tid) {
-  v = redux_fmax(v);
-  __syncthreads();
-  if ((tid & 31) == 0) red[tid >> 5] = v;
-  __syncthreads();
-  float m = 0.f;
-#pragma unroll
-  for (int w = 0; w < kShWarps; ++w) m = fmaxf(m, red[w]);
-  return m;
-}
 __device__ __forceinline__ float finite_abs(float v) {
   const float a = fabsf(v);
   return a < INFINITY ? a : 0.f;
@@ -574,7 +570,8 @@ __device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const S
   float* al = reinterpret_cast<float*>(sm + kAlOff);
   int* lim = reinterpret_cast<int*>(sm + kLimOff);
   volatile int* nvs = reinterpret_cast<volatile int*>(sm + kNvOff);
-  float* red = reinterpret_cast<float*>(sm + kRedOff);
+  float* sc = reinterpret_cast<float*>(sm + kScOff);
+  int* row_top = reinterpret_cast<int*>(sm + kAlOff);      // until the first raise: a row's largest magnitude
   auto bar = [&](int i) { return u32s(sm + kBarOff) + 8u * i; };
   const int rows = u.rows, S = u.S, tile0 = u.tile0, nt = u.nt, hkv = u.hkv;
 
@@ -593,16 +590,20 @@ __device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const S
   if (const int c = kShThreads - 1 - tid; c < N) {
     lim[c] = c < rows ? min(S, seq_vq(p, static_cast<int>(pair_of<N>(p, u, c) / p.Hq))) : INT_MAX;
     m_ref[c] = kUnset;
+    row_top[c] = 0;
   }
-  // the queries, scaled into fp16 (against the scales of the key groups): piece =
-  // 8 channels of a row
+  // The queries, scaled into fp16 by a power of two 2^kq (against the scales of the
+  // key groups): one for all rows while their largest magnitudes are within
+  // 2^kRowSpan of each other, else one per row, so that no row's magnitude costs
+  // another its bits. Piece = 8 channels of a row.
   int kq;
+  bool one_scale;
   {
     constexpr int PIECES = N * D / 8, PER = (PIECES + kShThreads - 1) / kShThreads;
-    float v[PER][8];
-    float top = 0.f;
+    float v[PER][8], top[PER];
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
+      top[k] = 0.f;
       const int f = tid + k * kShThreads, c = f / (D / 8), part = f % (D / 8);
       uint4 t = make_uint4(0u, 0u, 0u, 0u);
       if (f < PIECES && c < rows) t = *(reinterpret_cast<const uint4*>(p.q + pair_of<N>(p, u, c) * D) + part);
@@ -613,21 +614,35 @@ __device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const S
         const float2 a = bf16x2_to_float2(w[i]);
         v[k][2 * i] = a.x * f2;
         v[k][2 * i + 1] = a.y * f2;
-        top = fmaxf(top, fmaxf(finite_abs(v[k][2 * i]), finite_abs(v[k][2 * i + 1])));
+        top[k] = fmaxf(top[k], fmaxf(finite_abs(v[k][2 * i]), finite_abs(v[k][2 * i + 1])));
       }
     }
-    kq = scale_exp(block_max(top, red, tid));
-    const float f2 = pow2(kq);
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {                        // (magnitudes order as their bits do)
+      const int f = tid + k * kShThreads;
+      if (f < PIECES) atomicMax(row_top + f / (D / 8), __float_as_int(top[k]));
+    }
+    __syncthreads();
+    {
+      const int t0 = row_top[lane % N], t1 = row_top[(lane + 32) % N];
+      const int least = min(t0 > 0 ? t0 : INT_MAX, t1 > 0 ? t1 : INT_MAX);   // (zero rows fit any scale)
+      kq = scale_exp(__int_as_float(__reduce_max_sync(0xffffffffu, max(t0, t1))));
+      const int lo = __reduce_min_sync(0xffffffffu, least);
+      one_scale = lo == INT_MAX || scale_exp(__int_as_float(lo)) - kq <= kRowSpan;
+      if (const int c = kShThreads - 1 - tid; c < N) sc[c] = pow2(-scale_exp(__int_as_float(row_top[c])));
+    }
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
       const int f = tid + k * kShThreads, c = f / (D / 8), byte = (f % (D / 8)) * 16;
       if (f >= PIECES) continue;
+      const float f2 = pow2(one_scale ? kq : scale_exp(__int_as_float(row_top[c])));
       *reinterpret_cast<uint4*>(sm + kQOff + (byte >> 7) * (N * 128) + c * 128 + ((byte & 127) ^ ((c & 7) << 4))) =
           make_uint4(half2_bits(v[k][0] * f2, v[k][1] * f2), half2_bits(v[k][2] * f2, v[k][3] * f2),
                      half2_bits(v[k][4] * f2, v[k][5] * f2), half2_bits(v[k][6] * f2, v[k][7] * f2));
     }
   }
-  const float scale = ldexpf(p.scale_log2, -kq);
+  const float scale = one_scale ? ldexpf(p.scale_log2, -kq) : p.scale_log2;
   if constexpr (T::LB < 32) {
     for (int i = tid; i < kTileBytes / 16; i += kShThreads)
       *reinterpret_cast<uint4*>(sm + kVtileOff + i * 16) = make_uint4(0u, 0u, 0u, 0u);
@@ -801,6 +816,10 @@ __device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const S
       uint32_t sv[NC];
       tld<NC>(lanes + kTmS + (i & 1) * 64 + c0, sv);
       tld_wait();
+      if (!one_scale) {                                    // block-uniform; exact, but for scores out of float32's range
+#pragma unroll
+        for (int c = 0; c < NC; ++c) sv[c] = __float_as_uint(__uint_as_float(sv[c]) * sc[c0 + c]);
+      }
       if (nv < 32 && lane >= nv) {                         // no token in this slot
 #pragma unroll
         for (int c = 0; c < NC; ++c) sv[c] = 0xff800000u;

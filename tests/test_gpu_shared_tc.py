@@ -153,6 +153,23 @@ def test_one_row_far_above_the_others():
     check_shared(c, *c.run_gpu())
 
 
+@pytest.mark.parametrize("size", [1e9, 1e12, 3e38])
+@pytest.mark.parametrize("rows,h,kw", [(6, 16, {}), (20, 4, {}), (40, 2, {}), (6, 16, dict(head_dim=96, chan_group=8, page_tokens=96))])
+def test_a_row_does_not_depend_on_its_neighbours_magnitude(rows, h, kw, size):
+    # neighbours in one group: an empty sequence whose query was never written, a
+    # sequence of windows only and one with tokens, all of a huge finite size
+    c = SharedCase(shape(h, **kw), [(rows, 300)], [20, None, 64, 5.0] + [1, 2] * (rows // 2 - 2), seed=17)
+    clean, lse = c.run_gpu()
+    check_shared(c, clean, lse, pairs=sample_pairs(c.B, h, 20, 2, whole=(0, 1)))
+    g = torch.Generator().manual_seed(3)
+    for b in (1, 3, 4):
+        c.q[b] = (size * (0.5 + 0.5 * torch.rand(c.q[b].shape, generator=g))).to(torch.bfloat16)
+    out, lse2 = c.run_gpu()
+    keep = [b for b in range(c.B) if b not in (3, 4)]
+    np.testing.assert_array_equal(out[keep], clean[keep])
+    np.testing.assert_array_equal(lse2[keep], lse[keep])
+
+
 def test_infinite_and_nan_queries_spoil_their_own_rows_only():
     c = SharedCase(H16, [(6, 300)], [20, 3, 64, 0, 1, 2], seed=19)
     clean, lse = c.run_gpu()
