@@ -485,7 +485,7 @@ loopvq_status loopvq_prefill_attn(const loopvq_config* cfg, int layer, int loop_
  * Two forms, chosen per call:
  *  - bf16 output, (J, c) = (32, 4), (16, 4), (12, 8), (16, 8) or (24, 4), on
  *    average at least four query rows (sequences times Hq/Hkv) per group, at
- *    least 64 (sequence, query head) pairs, sm_scale in [2^-20, 2^20]: the
+ *    least 64 (sequence, query head) pairs, sm_scale in [2^-20, 2^12]: the
  *    tensor-core form. Shared tokens are dequantised once per group and kv-head. Codewords and softmax
  *    weights enter the products in fp16 (half a step is 2^-11 relative; both are
  *    scaled by powers of two first), sums are float32, so a score, and lse, is

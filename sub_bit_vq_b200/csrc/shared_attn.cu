@@ -97,6 +97,11 @@ constexpr int kTileRows = 128;            // token rows of a tile (4 index block
 constexpr int kMaxRows = 64;              // query rows of a block
 constexpr float kRaise = 14.f;            // log2: a weight reaches 2^14 at most
 constexpr float kTop = 6.f;               // log2: weight of the maximum after a raise
+// A record's o (the window's apart) is 2^-kRecExp of its weighted sum, weights up to
+// 2^14, so that it stays in float32 wherever a plain sum of values does; the merge
+// takes m and l to the same scale. (Done where the records are written it cost 9 us of
+// 187 with 256 sequences.)
+constexpr int kRecExp = 14;
 constexpr float kUnset = -1e30f;          // reference of a row that has seen no token
 // log2: how far the rows of a unit may differ and still share a scale. A row's
 // largest entry is then 2^5 at least in fp16, so what its smaller ones lose (half
@@ -165,7 +170,7 @@ struct SharedParams {
   const uint16_t* win_k;
   const uint16_t* win_v;
   const unsigned char* tables;    // [Hkv][K, V] fp16 tables of kTabBytes
-  const int* exps;                // [Hkv][K, V][32]: a group's table entries are scaled by 2^exps
+  const int* exps;                // [Hkv][K, V][32]: a group's table entries are scaled by 2^exps (V: + kRecExp)
   int2* seqs;                     // [B] shared and own quantised tokens of a sequence
   float* srec;                    // [pairs + shared_blocks * N][4 + d] records of the shared blocks
   float* orec;                    // [pairs][NC][4 + d] records of the own chunks
@@ -308,11 +313,11 @@ __device__ __forceinline__ float redux_fmax(float v) {
 // 2^k for -126 <= k <= 127.
 __device__ __forceinline__ float pow2(int k) { return __int_as_float((127 + k) << 23); }
 
-// Power of two that brings values of magnitude `top` just below 2^14 (1 for 0
-// or no finite value).
+// Power of two that brings values of magnitude `top` just below 2^14. For 0 (or
+// no finite value) the largest one: what a table of zeros is multiplied with then
+// counts least when the query's own scale is chosen.
 __device__ __forceinline__ int scale_exp(float top) {
-  if (!(top > 0.f)) return 0;
-  return max(-100, min(100, 13 - ilogbf(top)));
+  return top > 0.f ? min(126, 13 - ilogbf(top)) : 126;     // -114 for the largest floats
 }
 
 __device__ __forceinline__ float finite_abs(float v) {
@@ -485,9 +490,9 @@ __global__ void __launch_bounds__(kE) shared_table_kernel(const float* cb_k, con
     float top = 0.f;
 #pragma unroll
     for (int i = 0; i < kE / 32; ++i) top = fmaxf(top, red[k][i]);
-    const int ex = scale_exp(top);
+    const int add = kv ? kRecExp : 0, ex = min(scale_exp(top), 126 - add);
     const float f = pow2(ex);
-    if (e == 0) exps[(h * 2 + kv) * 32 + j0 + k] = ex;
+    if (e == 0) exps[(h * 2 + kv) * 32 + j0 + k] = ex + add;
 #pragma unroll
     for (int i = 0; i < C / 4; ++i) {
       w[k * (C / 2) + 2 * i] = half2_bits(v[k][i].x * f, v[k][i].y * f);
@@ -1296,7 +1301,7 @@ __device__ void own_chunk(const SharedParams& p, const uint8_t* pool_h, int b, i
     request(blk + 1, e_next);                              // lands under this block's values
     e_next = entry_of(blk + 2);
     const float x = valid ? ((acc[0] + acc[1]) + (acc[2] + acc[3])) * scale : -INFINITY;
-    const float mx = redux_fmax(x) - 14.f;
+    const float mx = redux_fmax(x) - kRaise;
     if (mx > m) {                                          // warp-uniform
       const float f = m == -INFINITY ? 0.f : fast_exp2(m - mx);
       l *= f;
@@ -1401,7 +1406,7 @@ __global__ void __launch_bounds__(kOwnWarps * 32, 1) shared_own_kernel(const Sha
                                      : (LOOPVQ_DECODE_STATUS_TIMEOUT | LOOPVQ_DECODE_STATUS_UNDRAINED));
       }
     }
-    const float unv = lane < J ? pow2(-__ldg(exk + 32 + lane)) : 0.f;  // of this lane's record channels
+    const float unv = lane < J ? pow2(-__ldg(exk + 32 + lane)) : 0.f;   // of this lane's record channels
     const uint8_t* pool_h = p.pool_lg + hkv * p.pool_stride_head;
     if (tid == 0) *next = th;
     __syncthreads();
@@ -1488,8 +1493,8 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(const SharedParams p)
       const float* rec = r < ns ? p.srec + (span.x + static_cast<int64_t>(r) * N) * RS : p.orec + (pair * p.NC + r - ns) * RS;
       const bool ok = r < ns + nc;
       if (ok) {
-        mr[k] = __ldcg(rec);
-        lr[k] = __ldcg(rec + 1);
+        mr[k] = __ldcg(rec) + (r == ns ? 0.f : static_cast<float>(kRecExp));   // (ns: the window)
+        lr[k] = __ldcg(rec + 1) * (r == ns ? 1.f : 1.f / (1 << kRecExp));
       }
 #pragma unroll
       for (int c = 0; c < NCH; ++c) {
@@ -1686,10 +1691,11 @@ SharedLayout make_layout(const Geometry& g, int batch, int max_own) {
 // 56/49, 151/92; 8 groups of 4 26/60, 58/89, 152/168. 40 heads of 96 (c = 8): of 4
 // 19/32, 31/38, 70/60; of 8 21/48, 33/58, 70/110. With few (sequence, head) pairs
 // the four launches cost more than they save: one head of 64, 16 sequences 15/13,
-// 18/17, 23/20. The factor of a score is sm_scale log2(e) 2^-kq, |kq| <= 100 (the
-// queries' power of two): outside 2^-20 .. 2^20 it could leave float32's range.
+// 18/17, 23/20. The factor of a score is sm_scale log2(e) 2^-kq, kq >= -114 (the
+// queries' power of two): with sm_scale outside 2^-20 .. 2^12 it could leave
+// float32's range.
 bool shared_attn_supported(const Geometry& g, int batch, int n_groups, int out_dtype, float sm_scale) {
-  if (!(sm_scale >= 0x1p-20f && sm_scale <= 0x1p20f)) return false;
+  if (!(sm_scale >= 0x1p-20f && sm_scale <= 0x1p12f)) return false;
   if (out_dtype != LOOPVQ_DTYPE_BF16 || n_groups == 0) return false;
   if (static_cast<int64_t>(batch) * (g.Hq / g.Hkv) < 4ll * n_groups || static_cast<int64_t>(batch) * g.Hq < 64) return false;
   switch (g.J * 100 + g.c) {

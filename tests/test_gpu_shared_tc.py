@@ -123,6 +123,28 @@ def test_groups_of_channels_of_different_size():
     check_shared(c, *c.run_gpu())
 
 
+@pytest.mark.parametrize("k_scale", [1e-6, 1e-8, 1e-20])
+@pytest.mark.parametrize("dead", [[3], [0, 5, 31], list(range(1, 32))])
+def test_groups_of_channels_without_any_value(dead, k_scale):
+    # key (and value) codewords of some channel groups are all zero, the others small,
+    # with queries as large as the small ones ask for: scores of order one
+    c = SharedCase(H16, [(4, 300)], [40, 2, 100, 0], q_scale=1.0 / k_scale, seed=26)
+    c.cb[:, :, :, 0] *= k_scale
+    c.cb[:, :, :, :, :, dead] = 0.0
+    c.win[0] = (c.win[0].float() * k_scale).to(torch.bfloat16)
+    check_shared(c, *c.run_gpu())
+
+
+@pytest.mark.parametrize("k_scale,v_scale", [(1e36, 1.0), (2e38, 1e36), (1e-36, 1e-30)])
+def test_codebooks_at_the_ends_of_float32(k_scale, v_scale):
+    c = SharedCase(H16, [(4, 300)], [40, 2, 100, 0], q_scale=min(1.0 / k_scale, 1e36), seed=27)
+    c.cb.clamp_(-1, 1)
+    c.cb[:, :, :, 0] *= k_scale
+    c.cb[:, :, :, 1] *= v_scale
+    c.win = [(w.float().clamp(-1, 1) * f).to(torch.bfloat16) for w, f in zip(c.win, (k_scale, v_scale))]
+    check_shared(c, *c.run_gpu())
+
+
 def _rows_of(c, code):
     """Gives every token of the shared prefix key code `code[token]` in all groups."""
     for h in range(c.shape.n_kv_heads):
