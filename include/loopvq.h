@@ -229,7 +229,7 @@ loopvq_status loopvq_encode(const loopvq_config* cfg, int layer, int loop_group_
 /*
  * Reads the encoder status word of the current device into *flags
  * (LOOPVQ_ENCODE_STATUS_* bits that any loopvq_encode, loopvq_encode_evict,
- * loopvq_kmeans_step or loopvq_append kernel set since the word was last
+ * loopvq_kmeans_step or loopvq_append(_ahead) kernel set since the word was last
  * cleared) and clears it when `clear` is nonzero. This call synchronises with the device (it
  * copies a device word to the host). A word of zero means every encode so
  * far wrote all of its indices.
@@ -262,8 +262,8 @@ loopvq_status loopvq_encode_evict(const loopvq_config* cfg, int n_tokens, const 
  * the windows push out for the encoder (airadar.tv, section "Utilisation":
  * the first PREFIX_TOKENS and the latest RECENT_TOKENS tokens stay in bf16).
  * One call does what a serving program does between its q/k/v projection and
- * loopvq_decode_attn (one token per sequence) or its prompt attention (a
- * chunk of tokens per sequence).
+ * loopvq_decode_attn (one token per sequence; with loopvq_append_ahead) or its
+ * prompt attention (a chunk of tokens per sequence).
  *
  * Row r of the call is token i = r - s of sequence b, where the sequence has
  * the rows [s, s + n): s = token_starts[b], n = token_starts[b+1] - s, or
@@ -280,7 +280,9 @@ loopvq_status loopvq_encode_evict(const loopvq_config* cfg, int n_tokens, const 
  *   -1 when row r pushes nothing out.
  * The staged rows and slot_mapping are what loopvq_encode_evict (up to 64
  * rows) and loopvq_encode (any number) take once the loop group's steps are
- * complete. Rows without a sequence (behind the last token_starts entry, or
+ * complete. Attention at the new lengths reads the staged tokens from the
+ * pool: a program that attends before it can encode them uses
+ * loopvq_append_ahead (below) instead. Rows without a sequence (behind the last token_starts entry, or
  * of a sequence with seq_lens[b] <= 0: a padded batch) write nothing but
  * slot_mapping[r] = -1; staging rows that nothing was pushed into keep their
  * contents.
@@ -327,6 +329,38 @@ loopvq_status loopvq_append(const loopvq_config* cfg, int layer, int loop_step, 
                             const int32_t* token_starts, const int32_t* seq_lens,
                             const int32_t* block_table, void* win_k, void* win_v, void* q_out,
                             void* evicted, int64_t* slot_mapping, void* stream);
+
+/*
+ * loopvq_append that stages each token stage_ahead rows before it leaves the
+ * window: row r at position p stages the token e = p - R + stage_ahead (from
+ * the window if it was cached before the call, from row
+ * r - R + stage_ahead of the call otherwise), and slot_mapping[r] is that
+ * token's slot. Everything else is as for loopvq_append, which is
+ * stage_ahead = 0.
+ *
+ * A decode step needs this form. With length N the attention calls read the
+ * tokens up to N - R - 1 from the pool, so the index of the last one has to be
+ * there before they run; but an index covers all loop steps of its group, so
+ * the rows that a step stages can be encoded after its last loop step only.
+ * With stage_ahead = A, rows staged up to length N and encoded reach token
+ * N - 1 - R + A, and any next step of up to A new tokens per sequence finds
+ * every token that it attends to, at each of its loop steps. So: A = 1 for
+ * one token per step, else the most tokens that a step may add; the same A
+ * from a sequence's first append on, the prompt's included; the staged rows
+ * encoded before the next step. (With A = 0 the staged rows are exactly what
+ * the windows lose: to put them back after a rejected draft, or to encode them
+ * when no attention at the new length comes first.)
+ *  stage_ahead  0 .. R. The page table names the pages of the staged tokens
+ *               too: up to A tokens past those that attention reads.
+ */
+loopvq_status loopvq_append_ahead(const loopvq_config* cfg, int layer, int loop_step, int batch,
+                                  int n_tokens, const void* q, int64_t q_token_stride, const void* k,
+                                  int64_t k_token_stride, const void* v, int64_t v_token_stride,
+                                  const float* rope, int n_positions, int rot_dim, int interleaved,
+                                  int stage_ahead, const int32_t* token_starts,
+                                  const int32_t* seq_lens, const int32_t* block_table, void* win_k,
+                                  void* win_v, void* q_out, void* evicted, int64_t* slot_mapping,
+                                  void* stream);
 
 /*
  * One weighted k-means (Lloyd) step on the codebooks of (layer,

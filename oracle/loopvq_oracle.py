@@ -517,17 +517,25 @@ def rotate_ref(x: np.ndarray, cos: np.ndarray, sin: np.ndarray, interleaved: boo
 
 
 def append_sequence_ref(window: np.ndarray, tokens: np.ndarray, length: int, prefix: int,
-                        recent: int) -> dict[int, tuple[int, np.ndarray]]:
+                        recent: int, ahead: int = 0) -> dict[int, tuple[int, np.ndarray]]:
     """Append ``tokens [n][H][d]`` one by one to ``window [H][P+R][d]`` (in
     place) of a sequence whose length counting them is ``length``. Returns,
     for each row that pushes a token out of the recent window, the pushed-out
-    token's position and value ``[H][d]``."""
+    token's position and value ``[H][d]``; with ``ahead > 0`` (up to
+    ``recent``), for each row the token that will be pushed out ``ahead`` rows
+    later, which the window then still holds."""
     gone = {}
     n = len(tokens)
     for i in range(n):
         p = length - n + i
         if p < prefix:
             window[:, p] = tokens[i]
+            continue
+        if ahead > 0:
+            window[:, prefix + (p - prefix) % recent] = tokens[i]
+            e = p - recent + ahead
+            if e >= prefix:
+                gone[i] = (e, np.array(window[:, prefix + (e - prefix) % recent]))
             continue
         if recent == 0:
             gone[i] = (p, np.array(tokens[i]))

@@ -92,6 +92,9 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.loopvq_append.restype = I
     lib.loopvq_append.argtypes = [cfgp, I, I, I, I, P, I64, P, I64, P, I64, P, I, I, I, P, P, P, P,
                                   P, P, P, P, P]
+    lib.loopvq_append_ahead.restype = I
+    lib.loopvq_append_ahead.argtypes = [cfgp, I, I, I, I, P, I64, P, I64, P, I64, P, I, I, I, I, P, P, P,
+                                        P, P, P, P, P, P]
     lib.loopvq_prefill_workspace_bytes.restype = SZ
     lib.loopvq_prefill_workspace_bytes.argtypes = [cfgp, I, I, I]
     lib.loopvq_prefill_attn.restype = I
@@ -123,7 +126,8 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
 _lib = _load()
 
 EXPORTED = ("loopvq_status_string", "loopvq_cache_layout", "loopvq_encode", "loopvq_encode_evict",
-            "loopvq_encode_status", "loopvq_append", "loopvq_prefill_workspace_bytes", "loopvq_prefill_attn",
+            "loopvq_encode_status", "loopvq_append", "loopvq_append_ahead", "loopvq_prefill_workspace_bytes",
+            "loopvq_prefill_attn",
             "loopvq_decode_workspace_bytes", "loopvq_decode_attn", "loopvq_decode_attn_noalloc",
             "loopvq_decode_shared_workspace_bytes", "loopvq_decode_attn_shared",
             "loopvq_bf16_decode_workspace_bytes", "loopvq_bf16_decode_attn",
@@ -289,14 +293,17 @@ def loopvq_append(cfg: LoopVQConfig, layer: int, loop_step: int, q: torch.Tensor
                   q_out: torch.Tensor | None, evicted: torch.Tensor,
                   token_starts: torch.Tensor | None = None, interleaved: bool = False,
                   block_table: torch.Tensor | None = None, slot_mapping: torch.Tensor | None = None,
-                  stream=None) -> None:
+                  stage_ahead: int = 0, stream=None) -> None:
     """Appends n tokens to the windows of (layer, loop_step). q ``[n][Hq][d]``,
     k, v ``[n][Hkv][d]`` bf16 (any token stride); rope float32
     ``[positions][rot_dim]`` (cosines, then sines) or None; seq_lens int32
     ``[B]`` counting the new tokens; win_k, win_v bf16 ``[B][Hkv][P+R][d]``;
     q_out bf16 ``[n][Hq][d]``; evicted bf16 ``[L][G][2][g][n][Hkv][d]``;
     token_starts int32 ``[B+1]`` or None (one token per sequence);
-    slot_mapping int64 ``[n]``, written (with block_table) when given."""
+    slot_mapping int64 ``[n]``, written (with block_table) when given.
+    stage_ahead (0 .. recent_tokens): stages the token that many rows ahead of
+    the one a row pushes out; a decode step whose attention follows needs its
+    largest number of new tokens per sequence here (``loopvq_append_ahead``)."""
     n, batch = k.shape[0], seq_lens.shape[0]
     hq, hkv, d = cfg.n_q_heads, cfg.n_kv_heads, cfg.head_dim
     bf16, int32 = torch.bfloat16, torch.int32
@@ -325,9 +332,9 @@ def loopvq_append(cfg: LoopVQConfig, layer: int, loop_step: int, q: torch.Tensor
         table_ptr = _dense("block_table", block_table, int32, (batch, cfg.max_pages_per_seq))
     _on_current_device("loopvq_append", q, k, v, rope, seq_lens, win_k, win_v, q_out, evicted,
                        token_starts, block_table, slot_mapping)
-    st = _lib.loopvq_append(
+    st = _lib.loopvq_append_ahead(
         cfg.c_ref(), layer, loop_step, batch, n, q_ptr, qs, k.data_ptr(), ks, v.data_ptr(), vs,
-        rope_ptr, positions, rot, interleaved, starts_ptr, lens_ptr, table_ptr, wk_ptr, wv_ptr, qo_ptr,
+        rope_ptr, positions, rot, interleaved, stage_ahead, starts_ptr, lens_ptr, table_ptr, wk_ptr, wv_ptr, qo_ptr,
         ev_ptr, slots_ptr, _stream(stream))
     _check("loopvq_append", st)
 

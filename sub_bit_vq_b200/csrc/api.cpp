@@ -233,6 +233,19 @@ loopvq_status loopvq_append(const loopvq_config* cfg, int layer, int loop_step, 
                             const int32_t* token_starts, const int32_t* seq_lens,
                             const int32_t* block_table, void* win_k, void* win_v, void* q_out,
                             void* evicted, int64_t* slot_mapping, void* stream) {
+  return loopvq_append_ahead(cfg, layer, loop_step, batch, n_tokens, q, q_token_stride, k, k_token_stride, v,
+                             v_token_stride, rope, n_positions, rot_dim, interleaved, 0, token_starts,
+                             seq_lens, block_table, win_k, win_v, q_out, evicted, slot_mapping, stream);
+}
+
+loopvq_status loopvq_append_ahead(const loopvq_config* cfg, int layer, int loop_step, int batch,
+                                  int n_tokens, const void* q, int64_t q_token_stride, const void* k,
+                                  int64_t k_token_stride, const void* v, int64_t v_token_stride,
+                                  const float* rope, int n_positions, int rot_dim, int interleaved,
+                                  int stage_ahead, const int32_t* token_starts,
+                                  const int32_t* seq_lens, const int32_t* block_table, void* win_k,
+                                  void* win_v, void* q_out, void* evicted, int64_t* slot_mapping,
+                                  void* stream) {
   Geometry g;
   loopvq_status st = loopvq::make_geometry(cfg, &g);
   if (st != LOOPVQ_OK) return st;
@@ -240,6 +253,7 @@ loopvq_status loopvq_append(const loopvq_config* cfg, int layer, int loop_step, 
   if (batch <= 0 || batch > g.max_batch || n_tokens < 0) return LOOPVQ_ERR_INVALID_ARG;
   if (rot_dim < 0 || rot_dim > g.d || rot_dim % 2 != 0 || n_positions < 0) return LOOPVQ_ERR_INVALID_ARG;
   if ((rot_dim > 0) != (rope != nullptr) || (rot_dim > 0 && n_positions == 0)) return LOOPVQ_ERR_INVALID_ARG;
+  if (stage_ahead < 0 || stage_ahead > g.R) return LOOPVQ_ERR_INVALID_ARG;
   if (rot_dim % 4 != 0) return LOOPVQ_ERR_UNSUPPORTED;
   if (n_tokens == 0) return LOOPVQ_OK;
   if (token_starts == nullptr && n_tokens != batch) return LOOPVQ_ERR_INVALID_ARG;
@@ -257,7 +271,7 @@ loopvq_status loopvq_append(const loopvq_config* cfg, int layer, int loop_step, 
     return LOOPVQ_ERR_INVALID_ARG;
   loopvq::AppendArgs a{&g,           layer,          loop_step, batch,          n_tokens,  q,
                        q_token_stride, k,            k_token_stride, v,         v_token_stride, rope,
-                       n_positions,  rot_dim,        interleaved, token_starts, seq_lens,  block_table,
+                       n_positions,  rot_dim,        interleaved, stage_ahead, token_starts, seq_lens, block_table,
                        win_k,        win_v,          q_out,     evicted,        slot_mapping, stream};
   return loopvq::launch_append(a);
 }

@@ -9,15 +9,18 @@
 //              rounding to bf16 (round to nearest even): every product and sum
 //              sees the table's 24 bits, and the cache holds bf16.
 //   windows    p < P goes to slot p, the last R tokens to P + (p - P) mod R.
-//   staging    the token e = p - R >= P that row r pushes out goes to row r of
-//              the staging slice: from the window when it was cached before
-//              the call (e < N_b - n_b), else from row r - R of the call.
+//   staging    the token e = p - R + A >= P, A rows ahead of the one that row r
+//              pushes out, goes to row r of the staging slice: from the window
+//              when it was cached before the call (e < N_b - n_b), else from row
+//              r - R + A of the call. (A = 1 in a decode step: the index of a token
+//              is in the pool before the token leaves the window.)
 //
-// A ring slot is read (its old token) by the first row of the call in its
-// residue class mod R and written by the last. Both are done by the thread of
-// the first row, which rotates the last row's token again for it (at most R
-// rows of a sequence): read and write stay in one thread, in order, and no
-// thread waits for another. Every other row writes only places of its own.
+// A ring slot that the call overwrites is read (its old token) by the first row of
+// the call in its residue class mod R and written by the last. Both are done by
+// the thread of the first row, which rotates the last row's token again for it (at
+// most R rows of a sequence): read and write stay in one thread, in order, and no
+// thread waits for another. Every other row writes only places of its own; what
+// the last A rows stage is in slots that the call leaves alone.
 //
 // Bound: HBM for prompts, the launch for a decode step. Each thread moves two
 // 16-byte chunks of a head's row at a time (the two that rotate together), so a
@@ -56,7 +59,7 @@ struct AppendParams {
   int64_t* slots;
   int* status;
   int batch, n_tokens, Hq, Hkv, d, P, R, Pg, n_pages, max_pages_per_seq;
-  int rot, n_positions, interleaved, units;
+  int rot, n_positions, interleaved, units, lead;   // lead: A
 };
 
 // Where a row belongs: sequence (-1: none, nothing is written for the row),
@@ -173,9 +176,9 @@ __device__ __forceinline__ RowInfo locate_row(const AppendParams& p, int r, int 
   return f;
 }
 
-// Pool slot of the token that the row pushes out, or -1.
+// Pool slot of the token that the row stages, or -1.
 __device__ __forceinline__ int64_t evicted_slot(const AppendParams& p, const RowInfo& f) {
-  const int v = f.p - p.R - p.P;          // its index among the quantised tokens
+  const int v = f.p - p.R + p.lead - p.P; // its index among the quantised tokens
   if (f.b < 0 || v < 0) return -1;
   const int page = v / p.Pg;
   int phys = -1;
@@ -189,9 +192,10 @@ __device__ __forceinline__ int64_t evicted_slot(const AppendParams& p, const Row
 
 // Thread = one unit (two chunks of V values that rotate together, or two
 // plain ones) of one head of the fused row [q heads][k heads][v heads]; it
-// walks the CTA's rows.
+// walks the CTA's rows. With eight rows seven blocks share an SM (72 registers; six
+// of 76: 143 us against 135 on 32768 tokens).
 template <int V, int ROWS>
-__global__ void __launch_bounds__(kApThreads) append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kApThreads, ROWS > 1 ? 7 : 1) append_kernel(const AppendParams p) {
   constexpr int kBatch = ROWS < 2 ? ROWS : 2;
   constexpr bool kStream = ROWS > 1;
   __shared__ RowInfo rows[ROWS];
@@ -253,21 +257,31 @@ __global__ void __launch_bounds__(kApThreads) append_kernel(const AppendParams p
     uint16_t* win = (is_v ? p.win_v : p.win_k) + (static_cast<int64_t>(f.b) * p.Hkv + h) * (p.P + p.R) * p.d;
     uint16_t* ev = (is_v ? p.ev_v : p.ev_k) + static_cast<int64_t>(h) * p.d;
     const int64_t ev_row = static_cast<int64_t>(p.Hkv) * p.d;
+    const int wait = p.R - p.lead;        // rows from a token to the one that stages it
     if (f.p < p.P)
       put(win + static_cast<int64_t>(f.p) * p.d, x);
-    else if (f.after >= p.R)              // pushed out by a later row of this call
-      put(ev + (r + p.R) * ev_row, x);
+    else if (f.after >= wait)             // staged by this or a later row of this call
+      put(ev + (r + wait) * ev_row, x);
+    // the staged token is one of the window that stays in it
+    if (f.after < p.lead && f.before < wait && f.p - wait >= p.P) {
+      const uint16_t* kept = win + static_cast<int64_t>(p.P + (f.p - wait - p.P) % p.R) * p.d;
+      Pair<V> old;
+      old.a = load_chunk<V, kStream>(kept + e0);
+      old.b = load_chunk<V, kStream>(kept + e1);
+      put(ev + r * ev_row, old);
+    }
     if (f.before >= p.R) return;          // (R = 0: every row)
-    // first row of its residue class: the old token of the ring slot goes to
-    // the staging row, the class's last token into the slot
+    // first row of its residue class: the old token of the ring slot goes to the
+    // row that stages it (unless an earlier call did), the class's last token into
+    // the slot
     const int ahead = f.after / p.R * p.R;
     if (f.p + ahead < p.P) return;
     uint16_t* slot = win + static_cast<int64_t>(p.P + (f.p + ahead - p.P) % p.R) * p.d;
-    if (f.p - p.R >= p.P) {
+    if (f.p - p.R >= p.P && f.before >= p.lead) {
       Pair<V> old;
       old.a = load_chunk<V, kStream>(slot + e0);
       old.b = load_chunk<V, kStream>(slot + e1);
-      put(ev + r * ev_row, old);
+      put(ev + (r - p.lead) * ev_row, old);
     }
     if (ahead > 0) {
       x = load(r + ahead);
@@ -326,6 +340,7 @@ loopvq_status launch_append(const AppendArgs& a) {
   p.rot = a.rot_dim;
   p.n_positions = a.n_positions;
   p.interleaved = a.interleaved;
+  p.lead = a.stage_ahead;
   // 16-byte chunks unless the rotated half is not a whole number of them
   const bool wide = a.rot_dim % 16 == 0;
   const int V = wide ? 8 : 2;

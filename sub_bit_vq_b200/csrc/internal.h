@@ -143,6 +143,7 @@ struct AppendArgs {
   int64_t v_token_stride;
   const float* rope;             // null when rot_dim is 0
   int n_positions, rot_dim, interleaved;
+  int stage_ahead;               // 0 .. R
   const int32_t* token_starts;   // or null: one token per sequence
   const int32_t* seq_lens;
   const int32_t* block_table;    // used with slot_mapping only

@@ -128,3 +128,30 @@ def test_rotation_oracle_is_a_rotation():
         z = (a + 1j * b) * np.exp(1j * ang)
         c, d = (y[:, 0:8:2], y[:, 1:8:2]) if inter else (y[:, :4], y[:, 4:8])
         np.testing.assert_allclose(c + 1j * d, z, atol=1e-14)
+
+
+@pytest.mark.parametrize("ahead", [0, 1, 64])
+def test_stage_ahead_is_checked(ahead):
+    a = dict(layer=0, loop=0, batch=2, n=0, q=0x1000, qs=768, k=0x2000, ks=384, v=0x3000, vs=384, rope=0x4000, pos=100,
+             rot=128, inter=0, ahead=ahead, starts=None, sl=0x5000, bt=0x6000, wk=0x7000, wv=0x8000, qo=0x9000, ev=0xA000,
+             slots=0xB000)
+    call = lambda **over: B.library().loopvq_append_ahead(ctypes.byref(_cfg().c_struct()), *{**a, **over}.values(), None)
+    assert call() == B.LOOPVQ_OK                 # (no tokens: no work)
+    assert call(ahead=-1) == call(ahead=65) == E
+    assert call(layer=2) == call(rot=-4) == E
+
+
+@pytest.mark.parametrize("P,R", [(8, 64), (0, 5), (3, 1)])
+def test_window_oracle_stages_ahead(P, R):
+    # every token once, in order, `ahead` rows before it leaves the window
+    for ahead in {1, (R + 1) // 2, R}:
+        win = np.full((1, P + R, 1), -1.0)
+        out, N = [], 0
+        for n in (1, 2, 70, 3, 200, 1, 64):
+            toks = np.arange(N, N + n, dtype=float).reshape(n, 1, 1)
+            N += n
+            for i, (pos, val) in sorted(O.append_sequence_ref(win, toks, N, P, R, ahead).items()):
+                assert val[0, 0] == pos == N - n + i - R + ahead
+                out.append(pos)
+            assert sorted(int(x) for x in win[0, :, 0] if x >= 0) == list(range(min(N, P))) + list(range(max(P, N - R), N))
+            assert out == list(range(P, max(P, N - R + ahead)))

@@ -320,3 +320,44 @@ def test_staged_rows_feed_the_encoder():
             for h in range(c.Hkv):
                 got = plane[h, s // c.page, kv, off]
                 assert (got == ref[n, h]).mean() > 0.96
+
+
+@pytest.mark.parametrize("ahead", [1, 3, 63, 64])
+@pytest.mark.parametrize("name", list(CASES))
+def test_staging_ahead_matches_the_oracle(name, ahead, monkeypatch):
+    c = Case(seed=len(name), **CASES[name])
+    ahead = min(ahead, c.R)
+    call, ref = L.loopvq_append, O.append_sequence_ref
+    monkeypatch.setattr(L, "loopvq_append", lambda *a, **kw: call(*a, stage_ahead=ahead, **kw))
+    monkeypatch.setattr(O, "append_sequence_ref", lambda *a: ref(*a, ahead=ahead))
+    c.check(c.run())
+
+
+def test_staging_ahead_of_a_chunk_by_chunk_prompt_stages_every_token_once():
+    # whatever the pieces, the staged rows are the tokens P, P + 1, .. in order
+    r = torch.Generator().manual_seed(2)
+    k = torch.randn(1, 400, 2, 128, generator=r).to(BF)
+    pieces = [1, 5, 70, 64, 3, 1, 1, 130, 63, 62]
+    for ahead in (0, 1, 5, 64):
+        cfg = L.LoopVQConfig(n_layers=1, n_kv_heads=2, n_q_heads=2, head_dim=128, n_loops=1, loop_group=1, chan_group=4,
+                             n_pages=8, max_batch=1, max_pages_per_seq=8)
+        win = [torch.zeros(1, 2, 72, 128, dtype=BF, device="cuda") for _ in range(2)]
+        bt = torch.arange(8, dtype=torch.int32, device="cuda").view(1, 8)
+        done, slot = [], []
+        N = 0
+        for n in pieces:
+            rows = k[0, N:N + n].cuda()
+            N += n
+            ev = torch.full((1, 1, 2, 1, n, 2, 128), float("nan"), dtype=BF, device="cuda")
+            sl = torch.zeros(n, dtype=torch.int64, device="cuda")
+            i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+            L.loopvq_append(cfg, 0, 0, None, rows, rows, None, i32([N]), *win, None, ev, token_starts=i32([0, n]),
+                            block_table=bt, slot_mapping=sl, stage_ahead=ahead)
+            keep = sl >= 0
+            assert torch.equal(ev[0, 0, 0, 0][keep], ev[0, 0, 1, 0][keep])
+            assert bool(torch.isnan(ev[0, 0, 0, 0][~keep]).all())          # rows without a staged token
+            done.append(ev[0, 0, 0, 0][keep])
+            slot += sl[keep].tolist()
+        m = N - 8 - 64 + ahead
+        assert slot == list(range(m))
+        assert torch.equal(torch.cat(done).cpu(), k[0, 8:8 + m])
