@@ -519,10 +519,14 @@ loopvq_status loopvq_prefill_attn(const loopvq_config* cfg, int layer, int loop_
  * Two forms, chosen per call:
  *  - bf16 output, (J, c) = (32, 4), (16, 4), (12, 8), (16, 8) or (24, 4), on
  *    average at least four query rows (sequences times Hq/Hkv) per group, at
- *    least 64 (sequence, query head) pairs, sm_scale in [2^-20, 2^12]: the
- *    tensor-core form. Shared tokens are dequantised once per group and kv-head. Codewords and softmax
- *    weights enter the products in fp16 (half a step is 2^-11 relative; both are
- *    scaled by powers of two first), sums are float32, so a score, and lse, is
+ *    least 64 (sequence, query head) pairs, sm_scale in [2^-20, 2^12], and
+ *    max_group, max_shared_len and max_own_len for which it is estimated to be
+ *    the faster one (many own tokens beside few shared ones or in few sequences
+ *    speak against it, so bounds close to the lengths in use choose best): the
+ *    tensor-core form. Shared tokens are dequantised once per group and kv-head.
+ *    Codewords and softmax weights enter the products in fp16 (half a step is
+ *    2^-11 relative; codewords are scaled by powers of two per channel group,
+ *    queries per row where rows differ), sums are float32, so a score, and lse, is
  *    within about 2^-11 sm_scale sum |q_i k_i|. group_starts that do not ascend
  *    inside [0, batch], or device values past a bound of the call, set
  *    LOOPVQ_DECODE_STATUS_BAD_GROUP, and what lies past the bound is left out.

@@ -460,7 +460,7 @@ loopvq_status loopvq_decode_attn_shared(const loopvq_config* cfg, int layer, int
                                                              max_own_len))
     return LOOPVQ_ERR_WORKSPACE;
   const int max_seq_len = loopvq::shared_max_seq_len(g, max_shared_len, max_own_len);
-  if (loopvq::shared_attn_supported(g, batch, n_groups, out_dtype, sm_scale)) {
+  if (loopvq::shared_attn_supported(g, batch, n_groups, max_group, max_shared_len, max_own_len, out_dtype, sm_scale)) {
     st = loopvq::decode_check(cfg, layer, loop_step, batch, 1, max_seq_len, q, pool, codebooks, block_table,
                               seq_lens, win_k, win_v, sm_scale, out_dtype, out, lse, workspace,
                               workspace_bytes, &g);

@@ -76,7 +76,8 @@ size_t prefill_tc_workspace_bytes(const Geometry& g, int batch, int n_queries, i
 loopvq_status launch_prefill_tc(const DecodeArgs& a, size_t workspace_bytes);
 
 // Decode attention of groups that share a quantised prefix on the tensor
-// cores (shared_attn.cu): bf16 outputs, head_dim a multiple of 16 up to 128.
+// cores (shared_attn.cu): bf16 outputs; (J, c) = (32, 4), (16, 4), (12, 8),
+// (16, 8) or (24, 4).
 struct SharedArgs {
   const Geometry* geo;
   int layer, loop_step, batch, n_groups, max_group, max_shared, max_own;
@@ -95,7 +96,8 @@ struct SharedArgs {
   void* workspace;
   void* stream;
 };
-bool shared_attn_supported(const Geometry& g, int batch, int n_groups, int out_dtype, float sm_scale);
+bool shared_attn_supported(const Geometry& g, int batch, int n_groups, int max_group, int max_shared, int max_own,
+                           int out_dtype, float sm_scale);
 size_t shared_attn_workspace_bytes(const Geometry& g, int batch, int max_own);
 loopvq_status launch_shared_attn(const SharedArgs& a);
 

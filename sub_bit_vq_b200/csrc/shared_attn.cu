@@ -1531,31 +1531,50 @@ constexpr int kPlanSms = 148;             // blocks that run at once (one per SM
 constexpr int kOwnChunk = 256;            // own tokens of a task at least, and chunks of a pair at most
 constexpr int kMaxChunks = 64;
 
-SharedPlan make_plan(const Geometry& g, int batch, int n_groups, int max_group, int max_shared, int max_own) {
-  SharedPlan q{};
+// Query rows of a block: the width whose row tiles cost least by the measured
+// times of a tile (SM cycles), and the row tiles of a kv-head. Of several groups the
+// host knows the largest and the sum: half a row tile of each is taken as empty.
+// (61 sequences in 7 uneven groups, 2 query heads a head: 65 us with 32 rows, 69 with
+// the 64 that the largest group fills.)
+struct RowTiles {
+  int N;
+  double units, t_tile;
+};
+RowTiles row_tiles(const Geometry& g, int batch, int n_groups, int max_group) {
   const int ratio = g.Hq / g.Hkv;
-  // Query rows of a block: the width whose row tiles cost least by the measured
-  // times of a tile (SM cycles). Of several groups the host knows the largest and
-  // the sum: half a row tile of each is taken as empty. (61 sequences in 7 uneven
-  // groups, 2 query heads a head: 65 us with 32 rows, 69 with the 64 that the
-  // largest group fills.)
-  const int64_t most = static_cast<int64_t>(max_group) * ratio, all = static_cast<int64_t>(batch) * ratio;
-  double units = 0, t_tile = 0;
+  const int64_t most = static_cast<int64_t>(max_group) * ratio;
+  const int64_t all = std::min<int64_t>(batch, static_cast<int64_t>(n_groups) * max_group) * ratio;
+  RowTiles q{};
   for (int n = 16; n <= kMaxRows; n *= 2) {
     const double cap = static_cast<double>(n_groups) * ((most + n - 1) / n);
     const double u = n_groups > 1 ? std::min(cap, std::max<double>(n_groups, 0.5 * n_groups + static_cast<double>(all) / n)) : cap;
     const double t = n == 16 ? 2200 : n == 32 ? 2500 : 3400;
-    if (q.N == 0 || u * t < units * t_tile) {
-      q.N = n;
-      units = u;
-      t_tile = t;
-    }
+    if (q.N == 0 || u * t < q.units * q.t_tile) q = RowTiles{n, u, t};
   }
-  units = max_shared > 0 ? units * g.Hkv : 0;
+  return q;
+}
+
+// Own tokens of a task, and tasks of a pair past its window's.
+struct Chunks {
+  int CH, n;
+};
+Chunks own_chunks(const Geometry& g, int batch, int max_own) {
+  Chunks q;
   q.CH = static_cast<int64_t>(batch) * g.Hq >= 512 ? 2 * kOwnChunk : kOwnChunk;
   auto chunks = [&] { return max_own / q.CH + (max_own % q.CH != 0 ? 1 : 0); };
   while (chunks() > kMaxChunks) q.CH *= 2;
-  q.NC = 1 + chunks();                                     // the window, and the chunks
+  q.n = chunks();
+  return q;
+}
+
+SharedPlan make_plan(const Geometry& g, int batch, int n_groups, int max_group, int max_shared, int max_own) {
+  SharedPlan q{};
+  const RowTiles r = row_tiles(g, batch, n_groups, max_group);
+  const double units = max_shared > 0 ? r.units * g.Hkv : 0, t_tile = r.t_tile;
+  const Chunks own = own_chunks(g, batch, max_own);
+  q.N = r.N;
+  q.CH = own.CH;
+  q.NC = 1 + own.n;                                        // the window, and the chunks
   // Both grids together fill the machine once. The own grid gets the number of
   // blocks with which the later of the two ends first, by measured times (SM
   // cycles): a tile; a block's 16 warps' way through a task each, which grows with
@@ -1682,26 +1701,62 @@ SharedLayout make_layout(const Geometry& g, int batch, int max_own) {
   return w;
 }
 
-}  // namespace
-
-// The shapes that the kernels take, where sharing pays: measured on B200 (16
-// heads of 128, own tokens 75 on average; these kernels / streaming each sequence,
-// us at 200, 4000 and 16000 shared tokens): groups of 3 sequences 29/18, 32/24,
-// 33/31; of 4 18/19, 22/25, 34/35; of 8 18/25, 22/30, 34/50; 8 groups of 2 24/33,
-// 56/49, 151/92; 8 groups of 4 26/60, 58/89, 152/168. 40 heads of 96 (c = 8): of 4
-// 19/32, 31/38, 70/60; of 8 21/48, 33/58, 70/110. With few (sequence, head) pairs
-// the four launches cost more than they save: one head of 64, 16 sequences 15/13,
-// 18/17, 23/20. The factor of a score is sm_scale log2(e) 2^-kq, kq >= -114 (the
-// queries' power of two): with sm_scale outside 2^-20 .. 2^12 it could leave
-// float32's range.
-bool shared_attn_supported(const Geometry& g, int batch, int n_groups, int out_dtype, float sm_scale) {
-  if (!(sm_scale >= 0x1p-20f && sm_scale <= 0x1p12f)) return false;
-  if (out_dtype != LOOPVQ_DTYPE_BF16 || n_groups == 0) return false;
-  if (static_cast<int64_t>(batch) * (g.Hq / g.Hkv) < 4ll * n_groups || static_cast<int64_t>(batch) * g.Hq < 64) return false;
+// Cost of a (query head, quantised token) pair in 10^-6 us on the whole machine,
+// measured over the calls of the rule below: in the decode kernels, and as an own
+// token of these.
+struct TokenCost {
+  double decode, own;
+};
+bool token_cost(const Geometry& g, TokenCost* t) {
   switch (g.J * 100 + g.c) {
-    case 3204: case 1604: case 1208: case 1608: case 2404: return true;
+    case 3204: *t = TokenCost{14.0, 33.0}; return true;
+    case 1604: *t = TokenCost{8.5, 21.0}; return true;
+    case 1208: *t = TokenCost{13.0, 38.0}; return true;
+    case 1608: *t = TokenCost{8.2, 21.0}; return true;
+    case 2404: *t = TokenCost{19.0, 33.0}; return true;
     default: return false;
   }
+}
+
+// The calls that the kernels take: the shapes and types that they implement, where
+// they are estimated to be faster than the decode kernels, which stream every
+// sequence's own row of the page table. Both estimates (us) are fits to 1590 calls
+// timed in both forms: 1 to 16 groups of 2 to 128 sequences and up to 120 without
+// a group, 0 to 32000 shared and 1 to 32000 own tokens, 4 to 40 heads, the five
+// shapes. They are off by a tenth on average and by less than a quarter in nine of
+// ten calls; the form that they choose takes 1.01 times the better one's time on
+// average, 1.4 times at worst (21 calls lose more than a fifth). What decides is own tokens, which cost more here, against the shared ones
+// and the 0.09 us a (sequence, query head) pair that they cost there, these kernels /
+// decode kernels, 16 heads of 128, at 1, 500, 2000, 8000 and 32000 own tokens: 4
+// sequences over 500 shared ones 18/19, 24/19, 30/24, 43/28, 80/48; 8 over 16000
+// 36/50, 36/50, 44/53, 67/61, 162/94; 32 over 2000 23/72, 36/78, 46/85, 131/125; 64
+// over none 16/71, 32/114, 66/136, 187/214. 40 heads of 96 (c = 8), 4 sequences over
+// 16000: 78/61. Near a tie (a twentieth) the call stays here. Fewer than four query
+// rows a group or 64 (sequence, query head) pairs were not fitted.
+bool shared_form_pays(const Geometry& g, int batch, int n_groups, int max_group, int max_shared, int max_own) {
+  TokenCost cost;
+  const double pairs = static_cast<double>(batch) * g.Hq;
+  if (static_cast<int64_t>(batch) * (g.Hq / g.Hkv) < 4ll * n_groups || pairs < 64 || !token_cost(g, &cost)) return false;
+  // (own tokens, and the shared ones of several groups, as if spread over the upper
+  // half of their range)
+  const double several = n_groups > 1 ? 0.75 : 1.0, shared = several * max_shared, own = 0.75 * max_own;
+  const RowTiles r = row_tiles(g, batch, n_groups, max_group);
+  const double tiles = max_shared > 0 ? r.units * g.Hkv * (several * (max_shared / (4 * g.LB) + 1) + kSetupTiles) : 0;
+  const double task = std::min(max_own, own_chunks(g, batch, max_own).CH) * 32.0 / g.LB;   // a task's way
+  const double here = 16 + 1.25 * tiles * r.t_tile / (kPlanSms * 1900.0) + pairs * own * cost.own * 1e-6 + 0.016 * task;
+  const double decode = 13.5 + 0.09 * pairs + pairs * (shared + own) * cost.decode * 1e-6;
+  return here <= 1.05 * decode;
+}
+
+}  // namespace
+
+// The factor of a score is sm_scale log2(e) 2^-kq, kq >= -114 (the queries' power of
+// two): with sm_scale outside 2^-20 .. 2^12 it could leave float32's range.
+bool shared_attn_supported(const Geometry& g, int batch, int n_groups, int max_group, int max_shared, int max_own,
+                           int out_dtype, float sm_scale) {
+  if (!(sm_scale >= 0x1p-20f && sm_scale <= 0x1p12f)) return false;
+  if (out_dtype != LOOPVQ_DTYPE_BF16 || n_groups == 0) return false;
+  return shared_form_pays(g, batch, n_groups, max_group, max_shared, max_own);
 }
 
 size_t shared_attn_workspace_bytes(const Geometry& g, int batch, int max_own) {

@@ -411,3 +411,40 @@ def test_a_decode_step_append_then_shared_attention():
         got = c.win[0][b, :, slot].double().numpy()
         assert np.all(np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -20 * np.max(np.abs(want)))
     check_shared(c, out, lse)
+
+
+def _same_as_decode(c, out):
+    """Whether bf16 outputs are loopvq_decode_attn's to the bit: the form of the decode
+    kernels (the tensor-core form rounds otherwise somewhere)."""
+    d, cfg, n = c.device(), c.config(), max(c.seq_lens)
+    ref = torch.empty(c.B, c.shape.n_q_heads, c.shape.head_dim, dtype=torch.bfloat16, device="cuda")
+    ws = workspace(L.loopvq_decode_workspace_bytes(cfg, c.B, n))
+    L.loopvq_decode_attn(cfg, 0, c.t, d["q"], d["pool"], d["codebooks"], d["block_table"], d["seq_lens"], d["win_k"],
+                         d["win_v"], ref, ws.t, n, sm_scale=c.sm_scale)
+    return bool(np.array_equal(ref.float().cpu().numpy(), out))
+
+
+DEEP = shape(40, head_dim=96, chan_group=8, page_tokens=96)
+FORMS = {   # far from the tie on both sides
+    "own_dominates": (H16, [(8, 512)], [8000, 100, 7000, 6000, 8000, 5000, 7900, 4000], True),
+    "one_pair_in_a_batch_of_others": (H16, [(2, 4032)], [50, 9] + [4000, 3900, 4032, 3000], True),
+    "forty_heads_of_a_group_of_four": (DEEP, [(4, 16032)], [60, 0, 50, 3], True),
+    "nothing_shared": (H16, [(40, 0)], [i * 3 % 90 for i in range(40)], False),
+    "nothing_shared_and_no_own": (H16, [(6, 0)], [0] * 6, False),
+    "nothing_shared_in_two_groups": (H16, [(9, 0), (5, 0)], [i * 31 % 300 for i in range(15)], False),
+    "long_prefix": (H16, [(8, 9024)], [500, 20, 600, 3, 1, 0, 44, 255], False),
+    "long_prefix_and_many_chunks": (H16, [(16, 60032)], [17000, 16640, 16500, 100, 0, 1] + [i * 37 % 500 for i in range(10)],
+                                    False),
+    "long_prefix_of_forty_heads": (DEEP, [(8, 6048)], [60, 0, 50, 3, 300, 299, 1, 2], False),
+}
+
+
+@pytest.mark.parametrize("name", list(FORMS))
+def test_the_form_follows_shared_and_own_tokens(name):
+    s, groups, own, decode = FORMS[name]
+    # (whole pages are shared, so no page has to be copied)
+    c = SharedCase(s, groups, own, seed=len(name), copy_pages=False)
+    assert all(n % s.page_tokens == 0 for _, n in groups)
+    out, lse = c.run_gpu()
+    check_shared(c, out, lse, pairs=sample_pairs(c.B, s.n_q_heads, 20, 3))
+    assert _same_as_decode(c, out) == decode
