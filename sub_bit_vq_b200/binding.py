@@ -276,6 +276,20 @@ def _dense(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple) -> int:
     return t.data_ptr()
 
 
+def _cache_arrays(cfg: LoopVQConfig, pool: torch.Tensor, codebooks: torch.Tensor) -> None:
+    """The pool and the codebooks are dense and hold what the layout of cfg
+    says (kept with the config, which is frozen)."""
+    size = cfg.__dict__.get("_sizes")
+    if size is None:
+        lay = loopvq_cache_layout(cfg)
+        size = (lay["pool_bytes"], lay["codebook_bytes"] // 4)
+        object.__setattr__(cfg, "_sizes", size)
+    for name, t, need in (("pool", pool, size[0]), ("codebooks", codebooks, size[1])):
+        if t.numel() < need or not t.is_contiguous():
+            raise ValueError(f"{name} must be dense with at least {need} elements, not {tuple(t.shape)}"
+                             f"{'' if t.is_contiguous() else ' with strides ' + str(t.stride())}")
+
+
 def _token_rows(name: str, x: torch.Tensor, shape: tuple) -> int:
     """Token stride of a bf16 ``[n][heads][d]`` tensor with dense rows."""
     if x.dtype is not torch.bfloat16:
@@ -490,6 +504,9 @@ def loopvq_decode_attn_shared(cfg: LoopVQConfig, layer: int, loop_step: int, q: 
         _dense("lse", lse, torch.float32, (batch, hq))
     _on_current_device("loopvq_decode_attn_shared", q, pool, codebooks, block_table, seq_lens,
                        group_starts, shared_lens, win_k, win_v, out, workspace, lse)
+    _cache_arrays(cfg, pool, codebooks)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be dense")
     st = _lib.loopvq_decode_attn_shared(
         cfg.c_ref(), layer, loop_step, batch, n_groups, max_group, max_shared_len, max_own_len, *args,
         sm_scale, odt, out.data_ptr(), _ptr(lse), workspace.data_ptr(),

@@ -2,6 +2,7 @@
 workspace sizes, the binding's checks."""
 
 import ctypes
+import dataclasses
 import os
 import random
 import re
@@ -96,6 +97,44 @@ def test_binding_checks_shapes_types_and_device():
                  dict(out=torch.zeros(4, 6, 256, dtype=bf)[:, :, ::2]), dict(lse=torch.zeros(4, 5))):
         with pytest.raises(ValueError):
             call(**over)
+
+
+def test_binding_checks_pool_codebooks_and_workspace(monkeypatch):
+    # sizes and density, before the call (the library, which would launch, is replaced)
+    cfg = _cfg()
+    lay = L.loopvq_cache_layout(cfg)
+    bf, i32 = torch.bfloat16, torch.int32
+    pool, cb = torch.zeros(lay["pool_bytes"], dtype=torch.uint8), torch.zeros(lay["codebook_bytes"] // 4)
+    called = []
+
+    class Lib:
+        @staticmethod
+        def loopvq_decode_attn_shared(*a):
+            called.append(a)
+            return 0
+
+    monkeypatch.setattr(B, "_on_current_device", lambda *a: None)
+    monkeypatch.setattr(B, "_lib", Lib)
+
+    def call(**over):
+        a = dict(q=torch.zeros(4, 6, 128, dtype=bf), pool=pool, codebooks=cb, block_table=torch.zeros(4, 5, dtype=i32),
+                 seq_lens=torch.zeros(4, dtype=i32), group_starts=torch.zeros(3, dtype=i32),
+                 shared_lens=torch.zeros(2, dtype=i32), win_k=torch.zeros(4, 3, 72, 128, dtype=bf),
+                 win_v=torch.zeros(4, 3, 72, 128, dtype=bf), out=torch.zeros(4, 6, 128, dtype=bf),
+                 workspace=torch.zeros(64, dtype=torch.uint8), max_group=3, max_shared_len=200, max_own_len=100, stream=0)
+        a.update(over)
+        L.loopvq_decode_attn_shared(dataclasses.replace(cfg), 0, 0, **a)
+
+    monkeypatch.setattr(B, "loopvq_cache_layout", lambda c: lay)
+    call()
+    assert len(called) == 1
+    for over in (dict(pool=pool[:-1]), dict(codebooks=cb[1:]), dict(pool=torch.zeros(2 * pool.numel(), dtype=torch.uint8)[::2]),
+                 dict(codebooks=cb.view(2, -1).t()), dict(workspace=torch.zeros(128, dtype=torch.uint8)[::2])):
+        with pytest.raises(ValueError, match="dense"):
+            call(**over)
+    assert len(called) == 1
+    call(pool=torch.zeros(1 + pool.numel(), dtype=torch.uint8))
+    assert len(called) == 2
 
 
 def test_status_bit_matches_the_header():
