@@ -29,7 +29,7 @@ bool mul_ok(int64_t a, int64_t b, int64_t* out) {
 
 int pages_for(const Geometry& g, int seq_len) {
   const int n_vq = seq_len > g.W ? seq_len - g.W : 0;
-  return (n_vq + g.Pg - 1) / g.Pg;
+  return n_vq / g.Pg + (n_vq % g.Pg != 0 ? 1 : 0);
 }
 
 }  // namespace

@@ -165,3 +165,12 @@ def test_a_group_is_a_part_of_the_batch_whatever_its_starts(tmp_path):
                     want = range(max(s, 0), max(max(s, 0), min(e, batch)))[:most]
                     assert 0 <= lo and 0 <= n <= most and lo + n <= batch, (s, e, batch, most, lo, n)
                     assert range(lo, lo + n) == want, (s, e, batch, most, lo, n)   # (empty ranges are equal)
+
+
+def test_the_longest_lengths_are_counted_in_pages_without_wrapping():
+    # 2^31 - 1 tokens and pages of 256: rounding up to pages must not wrap and pass
+    # for a short sequence
+    cfg = _cfg(page_tokens=256, prefix_tokens=0, recent_tokens=0)
+    st = B.library().loopvq_decode_attn(cfg.c_ref(), 0, 0, 4, 2 ** 31 - 1, 0x1000, 0x2000, 0x3000, 0x4000, 0x5000, None, None,
+                                        0.1, 0, 0x8000, None, 0x9000, 1 << 40, None)
+    assert st == E
