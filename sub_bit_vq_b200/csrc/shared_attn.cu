@@ -179,6 +179,7 @@ struct SharedParams {
   float* lse;
   int B, n_groups, Hq, Hkv, ratio, W, Pg, n_pages, max_pages_per_seq;
   int max_group, max_shared, max_own;
+  int max_vq;                     // tokens that a row of the page table names, or INT_MAX
   Walk* walks;                    // [shared_blocks] where each block starts
   int2* spans;                    // [pairs] first shared record of a row, and their number (N records apart)
   int NC, CH;                     // own records of a pair (window, chunks), tokens of a chunk
@@ -327,7 +328,7 @@ __device__ __forceinline__ float finite_abs(float v) {
 
 // Quantised tokens of sequence b.
 __device__ __forceinline__ int seq_vq(const SharedParams& p, int b) {
-  return max(0, min(max(0, __ldg(p.seq_lens + b)) - p.W, p.max_pages_per_seq * p.Pg));
+  return max(0, min(max(0, __ldg(p.seq_lens + b)) - p.W, p.max_vq));
 }
 
 // Group of sequence b (-1: none; else b is one of the rows that group_info
@@ -1807,6 +1808,7 @@ loopvq_status launch_shared_attn(const SharedArgs& a) {
   p.Pg = g.Pg;
   p.n_pages = g.n_pages;
   p.max_pages_per_seq = g.max_pages_per_seq;
+  p.max_vq = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(g.max_pages_per_seq) * g.Pg, INT_MAX));
   p.max_group = a.max_group;
   p.max_shared = a.max_shared;
   p.max_own = a.max_own;

@@ -413,6 +413,14 @@ def test_a_decode_step_append_then_shared_attention():
     check_shared(c, out, lse)
 
 
+def test_a_page_table_of_more_than_two_to_the_31_tokens():
+    # 2^23 entries a row for pages of 256: lengths are bounded by the table in 64 bits
+    c = SharedCase(shape(page_tokens=256), [(4, 300)], [40, 2, 100, 0], seed=33)
+    c.max_pages = 2 ** 23
+    c.bt = np.concatenate([c.bt, np.zeros((4, c.max_pages - c.bt.shape[1]), np.int32)], 1)
+    check_shared(c, *c.run_gpu())
+
+
 def _same_as_decode(c, out):
     """Whether bf16 outputs are loopvq_decode_attn's to the bit: the form of the decode
     kernels (the tensor-core form rounds otherwise somewhere)."""
