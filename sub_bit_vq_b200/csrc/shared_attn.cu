@@ -616,7 +616,7 @@ __device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const S
       const uint32_t w[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float f2 = pow2(f < PIECES ? -__ldg(exk + (part * 8 + 2 * i) / C) : 0);
+        const float f2 = pow2(f < PIECES ? -__ldcg(exk + (part * 8 + 2 * i) / C) : 0);
         const float2 a = bf16x2_to_float2(w[i]);
         v[k][2 * i] = a.x * f2;
         v[k][2 * i + 1] = a.y * f2;
@@ -925,7 +925,7 @@ __device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const S
     if (!failed) {
       // ---- the rows' records: o from TMEM (lane = channel), m and l ------------------
       tc_after();
-      const float unscale = row < D ? pow2(-__ldg(exk + 32 + row / C)) : 0.f;
+      const float unscale = row < D ? pow2(-__ldcg(exk + 32 + row / C)) : 0.f;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         const float t = warp_sum(l[c]);
@@ -1398,7 +1398,7 @@ __global__ void __launch_bounds__(kOwnWarps * 32, 1) shared_own_kernel(const Sha
     __syncthreads();                                       // the head before is done with tables and scales
     if (!failed) {
       if (tid < 2) request_table(p, sm, hkv, tid, bar);
-      if (tid < J) fk[tid] = pow2(-__ldg(exk + tid));
+      if (tid < J) fk[tid] = pow2(-__ldcg(exk + tid));
       failed = __syncthreads_or(!mbar_wait(bar, phase & 1, kShSpin));
       if (failed && tid == 0) {                            // no copy may outlive the block
         const bool drained = mbar_wait(bar, phase & 1, kShDrainSpin);
@@ -1407,7 +1407,7 @@ __global__ void __launch_bounds__(kOwnWarps * 32, 1) shared_own_kernel(const Sha
                                      : (LOOPVQ_DECODE_STATUS_TIMEOUT | LOOPVQ_DECODE_STATUS_UNDRAINED));
       }
     }
-    const float unv = lane < J ? pow2(-__ldg(exk + 32 + lane)) : 0.f;   // of this lane's record channels
+    const float unv = lane < J ? pow2(-__ldcg(exk + 32 + lane)) : 0.f;   // of this lane's record channels
     const uint8_t* pool_h = p.pool_lg + hkv * p.pool_stride_head;
     if (tid == 0) *next = th;
     __syncthreads();
@@ -1432,7 +1432,7 @@ __global__ void __launch_bounds__(kOwnWarps * 32, 1) shared_own_kernel(const Sha
         own_window<D>(p, static_cast<int64_t>(b) * p.Hkv + hkv, max(0, min(__ldg(p.seq_lens + b), p.W)), p.q + pair * D, rec, lane);
         continue;
       }
-      const int2 seq = __ldg(p.seqs + b);                  // its shared tokens, its own
+      const int2 seq = __ldcg(p.seqs + b);                  // its shared tokens, its own
       const int c0 = ck * p.CH;
       if (c0 >= seq.y) continue;                           // the merge does not read it
       const int t0 = seq.x + c0, t1 = t0 + min(seq.y - c0, p.CH);
