@@ -361,3 +361,100 @@ def test_staging_ahead_of_a_chunk_by_chunk_prompt_stages_every_token_once():
         m = N - 8 - 64 + ahead
         assert slot == list(range(m))
         assert torch.equal(torch.cat(done).cpu(), k[0, 8:8 + m])
+
+
+MANY = {   # eight rows per block: at least 16384 blocks of 128 units
+    "wide": dict(old=[300, 0, 71, 9], counts=[500, 400, 201, 0], d=256, c=8, rot=256, Hq=40, Hkv=40, tail=13),
+    "wide_half_interleaved_gqa": dict(old=[0, 90, 1000], counts=[1300, 66, 1400], d=128, rot=64, inter=True, Hq=64, Hkv=16, tail=3),
+    "narrow_interleaved": dict(old=[0, 90], counts=[400, 333], d=96, c=8, rot=36, inter=True, page=96, Hq=40, Hkv=40),
+    "narrow": dict(old=[65, 0, 8], counts=[700, 68, 601], rot=20, Hq=16, Hkv=16, tail=9),
+    "not_rotated_keys_only": dict(old=[0, 90], counts=[1300, 800], rot=0, with_q=False, fused=False, Hq=60, Hkv=60),
+}
+
+
+@pytest.mark.parametrize("ahead", [0, 1, 5])
+@pytest.mark.parametrize("name", list(MANY))
+def test_many_rows_match_the_oracle(name, ahead, monkeypatch):
+    kw = MANY[name]
+    c = Case(seed=len(name), n_layers=1, layer=0, T=2, g=2, loop=1, **kw)
+    units = -(-c.d // (16 if c.rot % 16 == 0 else 4))
+    assert c.n * -(-((c.Hq if c.q is not None else 0) + 2 * c.Hkv) * units // 128) >= 16384
+    call, ref = L.loopvq_append, O.append_sequence_ref
+    monkeypatch.setattr(L, "loopvq_append", lambda *a, **kw: call(*a, stage_ahead=ahead, **kw))
+    monkeypatch.setattr(O, "append_sequence_ref", lambda *a: ref(*a, ahead=ahead))
+    c.check(c.run())
+
+
+def run_flagged(c, flag, monkeypatch):
+    """c.run() of a call that has to set exactly this status (and to stay inside its
+    buffers, which run checks first)."""
+    read = L.loopvq_encode_status
+    with monkeypatch.context() as m:
+        m.setattr(L, "loopvq_encode_status", lambda clear=False: read(clear) ^ (0 if clear else flag))
+        out = c.run()
+    assert read(clear=True) == flag
+    return out
+
+
+def test_a_sequence_at_a_bad_position_writes_nothing(monkeypatch):
+    c = Case(old=[100, 90, 20], counts=[3, 2, 70])
+    c.rope = c.rope[:101]                                  # the first one reaches past the table
+    c.check(run_flagged(c, B.LOOPVQ_ENCODE_STATUS_BAD_POSITION, monkeypatch), skip=(0,))
+    c = Case(old=[100, 90, 20], counts=[3, 2, 70])
+    c.total[1] = 1                                         # shorter than its two rows
+    c.check(run_flagged(c, B.LOOPVQ_ENCODE_STATUS_BAD_POSITION, monkeypatch), skip=(1,))
+
+
+def test_a_bad_page_costs_the_slot_only(monkeypatch):
+    kw = dict(old=[200, 100, 300], counts=[1, 1, 1], one=True, seed=4)
+    good, bad = Case(**kw), Case(**kw)
+    bad.bt[0, 2] = bad.cfg.n_pages                         # v = 200 - 72 = 128: page 2
+    bad.bt[1, 0] = -1                                      # v = 28: page 0
+    out = run_flagged(bad, B.LOOPVQ_ENCODE_STATUS_BAD_SLOT, monkeypatch)
+    want = good.run()
+    good.check(want)
+    for k in ("q", "wk", "wv", "ev"):
+        assert torch.equal(out[k].t, want[k].t), k
+    assert out["slots"].t.tolist() == [-1, -1, int(want["slots"].t[2])]
+
+
+def test_a_replayed_graph_reads_the_lengths_of_the_replay():
+    c = Case(old=[364, 135, 64], counts=[5, 3, 80], seed=3)
+    out = c.run()
+    c.check(out)
+    (args, kw) = c.args
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        L.loopvq_append(*args, **kw)
+    c.old, c.total = [o - 64 for o in c.old], [t - 64 for t in c.total]
+    args[7].sub_(64)
+    for buf, first in ((args[8], c.win[0]), (args[9], c.win[1])):
+        buf.copy_(first)
+    args[10].fill_(7.0)
+    args[11].fill_(5.0)
+    g.replay()
+    torch.cuda.synchronize()
+    for name, buf in out.items():
+        buf.check(name)
+    c.check(out)
+    assert L.loopvq_encode_status() == 0
+
+
+def test_two_appends_at_once_on_two_streams():
+    cases = [Case(old=[300, 71, 0], counts=[5, 3, 80], seed=3), Case(old=[1, 2, 500, 90], counts=[100, 1, 7, 66], seed=6)]
+    outs = [c.run() for c in cases]
+    want = [{k: b.t.clone() for k, b in o.items()} for o in outs]
+    streams = [torch.cuda.Stream() for _ in cases]
+    for c, o in zip(cases, outs):
+        (args, kw) = c.args
+        args[8].copy_(c.win[0])
+        args[9].copy_(c.win[1])
+        args[11].fill_(5.0)
+    torch.cuda.synchronize()
+    for c, s in zip(cases, streams):
+        (args, kw) = c.args
+        L.loopvq_append(*args, stream=s, **kw)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        for k in w:
+            assert torch.equal(o[k].t, w[k]), k
