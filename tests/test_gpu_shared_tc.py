@@ -4,6 +4,7 @@ outputs. The bound is check_shared's; large cases check a sample of the pairs.
 """
 
 import ctypes
+import math
 import os
 
 import numpy as np
@@ -419,6 +420,47 @@ def test_a_page_table_of_more_than_two_to_the_31_tokens():
     c.max_pages = 2 ** 23
     c.bt = np.concatenate([c.bt, np.zeros((4, c.max_pages - c.bt.shape[1]), np.int32)], 1)
     check_shared(c, *c.run_gpu())
+
+
+def _rounded_codebooks(c):
+    """The case's codebooks as the tables hold them: per (head, K or V, channel group)
+    scaled by the power of two that brings the largest entry into [2^13, 2^14), rounded
+    to fp16, scaled back."""
+    cb = c.cb.double().numpy()                             # [1][H][G][2][g][J][E][c]
+    top = np.abs(cb).max(axis=(-1, -2), keepdims=True)
+    ex = 13 - np.floor(np.log2(top))
+    return torch.from_numpy((cb * 2.0 ** ex).astype(np.float16).astype(np.float64) * 2.0 ** -ex)
+
+
+def check_rounding(case, out, lse, pairs):
+    """bf16 outputs against the oracle over the rounded codebooks.
+
+    With the codewords' rounding in the oracle what is left is small. A score is off by
+    the additions alone: 128 of products of fp16 values (exact), each of which may drop
+    a whole step (2^-23) of the sum, and a few scalings: d = S (128 + 12) 2^-23. A weight
+    is off by a factor within e^(+-2d) of the softmax and by its own rounding to fp16
+    (2^-11) against an unrounded sum; weights below fp16's normal range and the fast
+    exponential are within 2^-15 together (see check_shared); the output's own
+    rounding is 2^-8."""
+    for b, h in pairs:
+        ref, lref, A, S = case.oracle(b, h)
+        dx = S * 140 * 2.0 ** -23
+        e = A * (math.expm1(2 * dx) + 2.0 ** -11 + 2.0 ** -15)
+        err = np.abs(out[b, h].astype(np.float64) - ref)
+        assert np.all(err <= e + 2.0 ** -8 * (np.abs(ref) + e)), (b, h, float(np.max(err)))
+        assert abs(float(lse[b, h]) - lref) <= dx + 2.0 ** -19 + 2.0 ** -23 * abs(lref), (b, h, float(lse[b, h]), lref)
+
+
+@pytest.mark.parametrize("q_scale", [1.0, 30.0])
+@pytest.mark.parametrize("kw,rows,own", [
+    (dict(), 9, 300), (dict(h=8, q=24), 7, 70), (dict(head_dim=64), 8, 150),
+    (dict(head_dim=96, chan_group=8, page_tokens=96), 8, 150), (dict(head_dim=96, page_tokens=96), 6, 90),
+    (dict(chan_group=8), 6, 90), (dict(h=4), 30, 60), (dict(h=2), 70, 60)])
+def test_outputs_are_what_the_documented_rounding_gives(kw, rows, own, q_scale):
+    c = SharedCase(shape(**{"h": 16, **kw}), [(rows, 700)], [i * 37 % own for i in range(rows)], q_scale=q_scale, seed=40)
+    out, lse = c.run_gpu()
+    c.cb = _rounded_codebooks(c)
+    check_rounding(c, out, lse, sample_pairs(c.B, c.shape.n_q_heads, 60, 4))
 
 
 def _same_as_decode(c, out):
