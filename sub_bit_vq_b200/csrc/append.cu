@@ -345,9 +345,9 @@ loopvq_status launch_append(const AppendArgs& a) {
   const bool wide = a.rot_dim % 16 == 0;
   const int V = wide ? 8 : 2;
   p.units = (g.d + 2 * V - 1) / (2 * V);
-  const int items = ((a.q != nullptr ? g.Hq : 0) + 2 * g.Hkv) * p.units;
-  const int tiles = (items + kApThreads - 1) / kApThreads;
-  if (tiles > 65535) return LOOPVQ_ERR_UNSUPPORTED;
+  const int64_t items = ((a.q != nullptr ? g.Hq : 0) + 2ll * g.Hkv) * p.units;
+  if (items > 65535ll * kApThreads) return LOOPVQ_ERR_UNSUPPORTED;   // the grid's y extent
+  const int tiles = static_cast<int>((items + kApThreads - 1) / kApThreads);
   cudaStream_t st = static_cast<cudaStream_t>(a.stream);
   // One row per block while all blocks fit the machine at once or nearly so
   // (latency counts), eight rows per block beyond: measured equal near 16K

@@ -155,3 +155,9 @@ def test_window_oracle_stages_ahead(P, R):
                 out.append(pos)
             assert sorted(int(x) for x in win[0, :, 0] if x >= 0) == list(range(min(N, P))) + list(range(max(P, N - R), N))
             assert out == list(range(P, max(P, N - R + ahead)))
+
+
+def test_more_heads_than_a_grid_holds_are_refused():
+    # 2^29 query heads of 8 units: the product must not wrap to a small grid that
+    # leaves the queries out
+    assert _raw(_cfg(n_q_heads=2 ** 29, n_kv_heads=2 ** 10), qs=0) == U
