@@ -84,9 +84,10 @@ enum {
    * outside its buffer; the access was skipped (never set by the default
    * build, whose indices are in range by construction) */
   LOOPVQ_DECODE_STATUS_RANGE = 4,
-  /* a bounded wait of the tensor-core prefill form (for the tensor cores or
-   * a bulk copy) gave up; the affected records are NaN and the call's
-   * outputs are not to be trusted */
+  /* a bounded wait of the tensor-core form of loopvq_prefill_attn or of
+   * loopvq_decode_attn_shared (for the tensor cores, a bulk copy or another
+   * warp) gave up; the affected records are NaN and the call's outputs are
+   * not to be trusted */
   LOOPVQ_DECODE_STATUS_TIMEOUT = 8,
   /* with LOOPVQ_DECODE_STATUS_TIMEOUT: the work in flight could not be
    * waited for before the kernel exited */

@@ -23,9 +23,9 @@ LIB = os.path.join(PKG, "libloopvq.so")
 
 # Test builds of the same sources: name -> extra nvcc flags. The range-check
 # build checks the decode kernel's indices against their buffers; the
-# short-wait build gives the tensor-core encoder no tries at all, so a test can
-# watch the encoder report a timeout (it then waits, bounded, for the
-# tensor cores before freeing their memory).
+# short-wait build gives the tensor-core encoder and the shared-prefix decode no
+# tries at all, so a test can watch them report a timeout (they then wait,
+# bounded, for the tensor cores before freeing their memory).
 VARIANTS = {
     "rangecheck": ["-DLOOPVQ_RANGE_CHECK"],
     "shortwait": ["-DLOOPVQ_TC_SPIN=0"],

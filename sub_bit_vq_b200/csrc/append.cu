@@ -26,11 +26,11 @@
 // 16-byte chunks of a head's row at a time (the two that rotate together), so a
 // warp's accesses are whole 128-byte lines; with many rows a block walks eight
 // of them, two rows' loads in flight per thread (one, four and eight in flight:
-// 133.7, 142.4 and 190 us against 132.9 on 32768 tokens: more registers, fewer
-// resident warps) and streams past the caches (138.4 us without the hints).
-// Measured on B200, 16 + 2 x 16 heads of 128: 32768 tokens in 132.9 us
-// (822 MB, 6.2 TB/s, 94% of the measured copy rate); one token of 8 and 256
-// sequences in 2.6 and 3.3 us.
+// 133.7, 142.4 and 190 us where two took 132.9, on 32768 tokens: more registers,
+// fewer resident warps) and streams past the caches (138.4 us without the hints).
+// Measured on B200, 16 + 2 x 16 heads of 128: 32768 tokens in 135 us
+// (822 MB, 6.1 TB/s, 93% of the measured copy rate); one token of 8 and 256
+// sequences in 2.5 and 3.2 us.
 
 #include "common.cuh"
 #include "encode_common.cuh"

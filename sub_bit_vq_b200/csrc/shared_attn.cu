@@ -52,10 +52,10 @@
 // 32696 tokens: 33.5 MB, 5 us); the products are small. What a tile costs is
 // shared-memory accesses: 2 x 32 KB of lookups, as much of stores, and the
 // products' reads, 1650 cycles of 128 bytes with 16 query rows, 1900 with 64.
-// Measured 2200 and 3400 (1900 MHz): 53 us for those 8 sequences, of which 47 in
+// Measured 2200 and 3400 (1900 MHz): 53 us for those 8 sequences, of which 48 in
 // the shared grid (7 of them before its first tile), 5 + 1 around it in the tables
 // and the merge, against 77.9 us when every sequence streams on its own; 256
-// sequences over 16312 tokens 187 us against 1313 (205 with the weights computed
+// sequences over 16312 tokens 188 us against 1313 (205 with the weights computed
 // only once P's buffer is free: with 64 rows there is one).
 //
 // What lost: the keys in two half tiles of M = 64 (71 us for the 8 sequences: a
@@ -980,11 +980,11 @@ __device__ bool shared_segment(const SharedParams& p, unsigned char* sm, const S
 // every block does the same work whatever the groups' sizes and lengths, and
 // meets one or a few units. Its records go to rows R + c*N .., R the rows of the
 // units before: since R and c both grow along the blocks, no two collide.
-// 16 x 32696 tokens of d = 128 with 8 rows on 140 blocks: 47.5 us, 36 MB from HBM
+// 16 x 32696 tokens of d = 128 with 8 rows on 140 blocks: 47.9 us, 36 MB from HBM
 // (0.75 TB/s: not the bound), shared-memory lookups and stores at 44% of an SM's
 // rate and the products' reads at 26% by their bytes; the rest is the hand-over
 // between fill, products and softmax. With 64 rows on 100 blocks, 16312 tokens of
-// 16 heads and 4 row tiles: 162 us.
+// 16 heads and 4 row tiles: 159 us.
 template <int J, int C, int N>
 __global__ void __launch_bounds__(kShThreads, 1) shared_prefix_kernel(const SharedParams p) {
   using T = Shape<J, C>;
@@ -1528,7 +1528,7 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(const SharedParams p)
 struct SharedPlan {
   int N, NC, CH, shared_blocks, own_blocks;
 };
-constexpr int kPlanSms = 148;             // blocks that run at once (one per SM of a B200)
+constexpr int kPlanSms = 148;             // blocks that run at once (one per SM of a B200; fewer SMs take waves)
 constexpr int kOwnChunk = 256;            // own tokens of a task at least, and chunks of a pair at most
 constexpr int kMaxChunks = 64;
 
