@@ -496,8 +496,9 @@ loopvq_status loopvq_prefill_attn(const loopvq_config* cfg, int layer, int loop_
  * reach those tokens, the pages hold the same indices (usually they are the
  * same pages; a page that the prefix ends in may be each sequence's own copy).
  * The call reads them through the first sequence's row of block_table, which
- * names the pages of all shared_lens[i] tokens whatever its own length. The
- * remaining quantised tokens are read through each sequence's own row, the
+ * names the pages of all shared_lens[i] tokens whatever its own length, or, in
+ * the second form below, through each sequence's own row, which names them as far
+ * as the sequence has them. The remaining quantised tokens are read through each sequence's own row, the
  * bf16 windows from each sequence's own slots. A sequence in no group shares
  * nothing; one with fewer quantised tokens than shared_lens[i] uses the first
  * of them.

@@ -1757,6 +1757,10 @@ bool shared_attn_supported(const Geometry& g, int batch, int n_groups, int max_g
                            int out_dtype, float sm_scale) {
   if (!(sm_scale >= 0x1p-20f && sm_scale <= 0x1p12f)) return false;
   if (out_dtype != LOOPVQ_DTYPE_BF16 || n_groups == 0) return false;
+  // (records, tasks and a sequence's tokens are counted in 32 bits)
+  if (static_cast<int64_t>(batch) * g.Hq * (1 + own_chunks(g, batch, max_own).n) > INT_MAX / 2 ||
+      static_cast<int64_t>(max_shared) + max_own > INT_MAX / 2)
+    return false;
   return shared_form_pays(g, batch, n_groups, max_group, max_shared, max_own);
 }
 
@@ -1767,10 +1771,6 @@ size_t shared_attn_workspace_bytes(const Geometry& g, int batch, int max_own) {
 loopvq_status launch_shared_attn(const SharedArgs& a) {
   const Geometry& g = *a.geo;
   const SharedPlan q = make_plan(g, a.batch, a.n_groups, a.max_group, a.max_shared, a.max_own);
-  // (records, tasks and a sequence's tokens are counted in 32 bits)
-  if (static_cast<int64_t>(a.batch) * g.Hq * q.NC > INT_MAX / 2 ||
-      static_cast<int64_t>(a.max_shared) + a.max_own > INT_MAX / 2)
-    return LOOPVQ_ERR_UNSUPPORTED;
   const int gamma = a.loop_step / g.g, tau = a.loop_step % g.g;
   SharedParams p{};
   p.q = static_cast<const uint16_t*>(a.q);

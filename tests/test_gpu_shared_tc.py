@@ -422,6 +422,15 @@ def test_a_page_table_of_more_than_two_to_the_31_tokens():
     check_shared(c, *c.run_gpu())
 
 
+@pytest.mark.parametrize("bounds", [(4, 2 ** 30, 100), (4, 300, 2 ** 30), (4, 2 ** 31 - 1, 2 ** 31 - 1)])
+def test_bounds_as_loose_as_a_huge_page_table(bounds):
+    # counts that the tensor-core form does not hold take the decode kernels
+    c = SharedCase(shape(page_tokens=256), [(4, 300)], [40, 2, 100, 0], seed=33)
+    c.max_pages = 2 ** 23
+    c.bt = np.concatenate([c.bt, np.zeros((4, c.max_pages - c.bt.shape[1]), np.int32)], 1)
+    check_shared(c, *c.run_gpu(bounds=bounds))
+
+
 def _rounded_codebooks(c):
     """The case's codebooks as the tables hold them: per (head, K or V, channel group)
     scaled by the power of two that brings the largest entry into [2^13, 2^14), rounded
