@@ -458,3 +458,23 @@ def test_two_appends_at_once_on_two_streams():
     for o, w in zip(outs, want):
         for k in w:
             assert torch.equal(o[k].t, w[k]), k
+
+
+def test_the_c_call_without_staging_ahead_is_the_same_call():
+    c = Case(old=[300, 71, 0], counts=[5, 3, 80], seed=3)
+    out = c.run()
+    want = {k: b.t.clone() for k, b in out.items()}
+    (args, kw) = c.args
+    _, layer, loop, q, k, v, rope, lens, wk, wv, qo, ev = args
+    wk.copy_(c.win[0])
+    wv.copy_(c.win[1])
+    qo.fill_(7.0)
+    ev.fill_(5.0)
+    p = lambda t: t.data_ptr()
+    st = B.library().loopvq_append(c.cfg.c_ref(), layer, loop, c.B, c.n, p(q), q.stride(0), p(k), k.stride(0), p(v),
+                                   v.stride(0), p(rope), *rope.shape, 0, p(kw["token_starts"]), p(lens), p(kw["block_table"]),
+                                   p(wk), p(wv), p(qo), p(ev), p(kw["slot_mapping"]), torch.cuda.current_stream().cuda_stream)
+    assert st == B.LOOPVQ_OK
+    torch.cuda.synchronize()
+    for name in want:
+        assert torch.equal(out[name].t, want[name]), name
